@@ -478,6 +478,92 @@ int moe_backward(const moe_config_t* cfg,
                  float* dg_out, float* dlogits_out,
                  void* ws, cudaStream_t stream);
 
+/* ===========================================================================
+ * Around the layer: the block's norms, the optimizer step, and the experts'
+ * products in 8-bit integers.  The pages name these without fixing them:
+ * a mixture layer stands in a block with a norm before it and a residual
+ * sum after it ([8MOE] Switch Transformers, [STA324 §8.1]); its gradients
+ * end in an optimizer step; a trained layer is served at low precision.
+ * Their conventions are those at the top of this header.
+ * ======================================================================== */
+
+enum { MOE_RMSNORM = 0, MOE_LAYERNORM = 1 };     /* moe_norm_config_t.norm */
+
+/*
+ * Block norm configuration.  With N(v) = v / sqrt(mean(v^2) + eps)
+ * (MOE_RMSNORM) or (v - mean(v)) / sqrt(var(v) + eps) (MOE_LAYERNORM):
+ *   z     = N(y) * w_post + b_post        (w_post NULL: z = y)
+ *   r_out = r + alpha * gate * z          (gate NULL: 1)
+ *   x     = N(r_out) * w_pre + b_pre      r_out as stored (resid type)
+ *   dtype   type of y, x and their gradients; resid: type of the residual
+ *           stream r, r_out and its gradients (MOE_FP32 or MOE_BF16; resid
+ *           MOE_BF16 needs dtype MOE_BF16)
+ *   gate_len  tokens that share a row of `gate`: token t takes row
+ *           t / gate_len of [ceil(T / gate_len), D] (a sequence's gate, or
+ *           with gate_len = T one gate for all); 0: no gate
+ * Limits: T >= 1, 8 <= D <= 8192, D % 8 == 0; eps > 0.  Sums and
+ * statistics are fp32.
+ */
+typedef struct {
+  int32_t T, D;
+  int32_t norm;          /* MOE_RMSNORM, MOE_LAYERNORM */
+  int32_t dtype, resid;
+  int32_t gate_len;
+  float eps, alpha;
+} moe_norm_config_t;
+
+/*
+ * moe_block_norm — the norm after a block, its gate and residual scale, the
+ * residual sum, and the norm before the next block, in one pass.
+ *   r       [T,D] resid: residual stream before the block
+ *   y       [T,D] act: the block's output, or NULL: x = N(r) * w_pre + b_pre
+ *           alone (before the first block; w_post, b_post, gate and r_out
+ *           are then NULL)
+ *   w_post, b_post  [D] f32 or NULL (b_post needs w_post)
+ *   gate    [ceil(T/gate_len), D] f32; NULL if and only if gate_len = 0 or y is NULL
+ *   w_pre, b_pre    [D] f32 or NULL (w_pre NULL: r_out only, x is NULL;
+ *           b_pre needs w_pre; MOE_RMSNORM and MOE_LAYERNORM both take
+ *           biases)
+ *   r_out   [T,D] resid out (may be r itself)
+ *   x       [T,D] act out
+ *   stats   [T,4] f32 out or NULL: mean and 1/sqrt of y's norm, mean and
+ *           1/sqrt of r_out's (means 0 for MOE_RMSNORM; 0 and 1 for a norm
+ *           that is off), for moe_block_norm_backward
+ * Every tensor of T rows starts on a 16-byte boundary, and so do the
+ * vectors (MOE_ERR_ARG otherwise, with nothing launched).
+ */
+int moe_block_norm(const moe_norm_config_t* cfg, const void* r, const void* y,
+                   const float* w_post, const float* b_post, const float* gate,
+                   const float* w_pre, const float* b_pre, void* r_out, void* x,
+                   float* stats, cudaStream_t stream);
+
+/* Workspace of moe_block_norm_backward (256-byte aligned base).  Host-only;
+ * 0 for an invalid cfg. */
+int64_t moe_block_norm_ws_bytes(const moe_norm_config_t* cfg);
+
+/*
+ * moe_block_norm_backward — every gradient of moe_block_norm.
+ *   r_out, y, w_post, b_post, gate, w_pre, stats  as the forward had and left
+ *           them (r_out: the stream the second norm read; with y NULL, r)
+ *   dx      [T,D] act: gradient of x (NULL if and only if w_pre is NULL)
+ *   dr_out  [T,D] resid: gradient of r_out from its other readers, or NULL (0)
+ *   dy      [T,D] act out: gradient of y (NULL if and only if y is NULL)
+ *   dr      [T,D] resid out: gradient of r (may be dr_out itself)
+ *   dw_post, db_post, dw_pre, db_pre  [D] f32 out, dgate as gate, f32 out:
+ *           each may be NULL (not computed); with its parameter NULL it has
+ *           to be, but db_pre and db_post are also given to callers whose
+ *           biases are zero
+ *   ws      workspace (moe_block_norm_ws_bytes); calls that overlap on the
+ *           GPU need a workspace each
+ * The sums over tokens run in a fixed order: deterministic, no atomics.
+ */
+int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* r_out, const void* y,
+                            const float* w_post, const float* b_post, const float* gate,
+                            const float* w_pre, const float* stats, const void* dx,
+                            const void* dr_out, void* dy, void* dr, float* dw_post,
+                            float* db_post, float* dgate, float* dw_pre, float* db_pre,
+                            void* ws, cudaStream_t stream);
+
 /* Synchronises `stream`, reads and clears the device error word (bits in
  * *bits if non-NULL).  MOE_OK, MOE_ERR_DEVICE or MOE_ERR_CUDA. */
 int moe_check_status(cudaStream_t stream, uint32_t* bits);

@@ -11,7 +11,8 @@ from .api import (MoEError, MoeConfig, MoeSizes, config_from, make_config,
                   moe_router, moe_set_side_streams, moe_aux_loss_seq, moe_bias_update,
                   moe_route_expert_choice, moe_expert_ffn_gather,
                   moe_expert_ffn_combine, moe_aux_stats, moe_aux_loss_global,
-                  moe_set_backward_streams)
+                  moe_set_backward_streams, NormConfig, make_norm_config, moe_block_norm,
+                  moe_block_norm_backward, moe_block_norm_ws_bytes)
 from .layer import MoELayer
 
 __all__ = ["MoEError", "MoeConfig", "MoeSizes", "config_from", "make_config",
@@ -20,4 +21,5 @@ __all__ = ["MoEError", "MoeConfig", "MoeSizes", "config_from", "make_config",
            "moe_router", "moe_set_side_streams", "moe_aux_loss_seq", "moe_bias_update",
            "moe_route_expert_choice", "moe_expert_ffn_gather",
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
-           "moe_set_backward_streams", "MoELayer"]
+           "moe_set_backward_streams", "NormConfig", "make_norm_config", "moe_block_norm",
+           "moe_block_norm_backward", "moe_block_norm_ws_bytes", "MoELayer"]

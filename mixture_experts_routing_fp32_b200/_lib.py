@@ -17,6 +17,7 @@ MOE_FP32, MOE_BF16 = 0, 1
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 MOE_GMAX, MOE_GTOP2SUM = 0, 1
 MOE_GEMM_AUTO, MOE_GEMM_SIMT = 0, 1
+MOE_RMSNORM, MOE_LAYERNORM = 0, 1
 DEVERR_EXPERT_ID, DEVERR_TIMEOUT, DEVERR_ROWS = 1, 2, 4
 
 c_int32, c_int64, c_float, c_void_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
@@ -30,7 +31,8 @@ EXPORTS = ("moe_get_sizes", "moe_router", "moe_dispatch", "moe_aux_loss",
            "moe_dispatch_static", "moe_set_side_streams", "moe_aux_loss_seq",
            "moe_bias_update", "moe_route_expert_choice", "moe_expert_ffn_gather",
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
-           "moe_set_backward_streams")
+           "moe_set_backward_streams",
+           "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_ws_bytes")
 
 
 class MoeConfig(ctypes.Structure):
@@ -49,6 +51,12 @@ class MoeSizes(ctypes.Structure):
     _fields_ = [("rows_max", c_int64), ("tiles_max", c_int64),
                 ("capacity", c_int64), ("ws_bytes", ctypes.c_size_t),
                 ("row_align", c_int64)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("D", c_int32), ("norm", c_int32), ("dtype", c_int32),
+                ("resid", c_int32), ("gate_len", c_int32), ("eps", c_float),
+                ("alpha", c_float)]
 
 
 class MoEError(RuntimeError):
@@ -70,6 +78,7 @@ def lib():
     L = ctypes.CDLL(LIB_PATH)
     P = c_void_p
     cfg = ctypes.POINTER(MoeConfig)
+    norm = ctypes.POINTER(NormConfig)
     sig = {
         "moe_get_sizes": [cfg, ctypes.POINTER(MoeSizes)],
         "moe_router": [cfg, P, P, P, P, P, P, P, P, P, P, P, P],
@@ -99,6 +108,9 @@ def lib():
         "moe_aux_stats": [cfg, P, P, P, P, P],
         "moe_aux_loss_global": [cfg, P, P, P, P],
         "moe_set_backward_streams": [P],
+        "moe_block_norm": [norm] + [P] * 11,
+        "moe_block_norm_backward": [norm] + [P] * 18,
+        "moe_block_norm_ws_bytes": [norm],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -107,6 +119,7 @@ def lib():
     L.moe_status_string.restype = ctypes.c_char_p
     L.moe_launch_count.restype = ctypes.c_int64
     L.moe_profile_name.restype = ctypes.c_char_p
+    L.moe_block_norm_ws_bytes.restype = ctypes.c_int64
     _lib = L
     return L
 

@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from ._lib import MoeConfig, MoeSizes, MoEError, check, lib
+from ._lib import MoeConfig, MoeSizes, MoEError, NormConfig, check, lib
 from . import _lib as C
 
 
@@ -176,6 +176,46 @@ def moe_backward(cfg, x, w_r, logits, probs, lse, topk_idx, topk_w, counts,
         "moe_backward")
 
 
+def _dtype(name) -> int:
+    return C.MOE_BF16 if name in ("bf16", torch.bfloat16) else C.MOE_FP32
+
+
+def make_norm_config(T, D, *, norm="rms", dtype="bf16", resid=None, eps=1e-5, alpha=1.0,
+                     gate_len=0) -> NormConfig:
+    """Norm before / after a block (norm: "rms" or "layer"; resid: type of the
+    residual stream, that of the activations by default)."""
+    kinds = {"rms": C.MOE_RMSNORM, "layer": C.MOE_LAYERNORM}
+    if norm not in kinds:
+        raise MoEError("norm is 'rms' or 'layer', not %r" % (norm,))
+    return NormConfig(T=T, D=D, norm=kinds[norm], dtype=_dtype(dtype),
+                      resid=_dtype(dtype if resid is None else resid), gate_len=gate_len,
+                      eps=eps, alpha=alpha)
+
+
+def moe_block_norm(cfg, r, y, w_post, b_post, gate, w_pre, b_pre, r_out, x, stats,
+                   stream=None):
+    """r_out = r + alpha gate N(y); x = N(r_out) (y None: x = N(r) alone)."""
+    check(lib().moe_block_norm(ctypes.byref(cfg), _p(r), _p(y), _p(w_post), _p(b_post),
+                               _p(gate), _p(w_pre), _p(b_pre), _p(r_out), _p(x), _p(stats),
+                               _s(stream)), "moe_block_norm")
+
+
+def moe_block_norm_ws_bytes(cfg) -> int:
+    """Workspace of moe_block_norm_backward."""
+    n = int(lib().moe_block_norm_ws_bytes(ctypes.byref(cfg)))
+    if n <= 0:
+        check(C.MOE_ERR_ARG, "moe_block_norm_ws_bytes")
+    return n
+
+
+def moe_block_norm_backward(cfg, r_out, y, w_post, b_post, gate, w_pre, stats, dx, dr_out, dy,
+                            dr, dw_post, db_post, dgate, dw_pre, db_pre, ws, stream=None):
+    check(lib().moe_block_norm_backward(
+        ctypes.byref(cfg), _p(r_out), _p(y), _p(w_post), _p(b_post), _p(gate), _p(w_pre),
+        _p(stats), _p(dx), _p(dr_out), _p(dy), _p(dr), _p(dw_post), _p(db_post), _p(dgate),
+        _p(dw_pre), _p(db_pre), _p(ws), _s(stream)), "moe_block_norm_backward")
+
+
 def moe_check_status(stream=None) -> int:
     bits = ctypes.c_uint32(0)
     rc = lib().moe_check_status(_s(stream), ctypes.byref(bits))
@@ -233,4 +273,5 @@ __all__ = ["LaunchProfile", "MoEError", "MoeConfig", "MoeSizes", "make_config", 
            "moe_launch_count", "moe_set_side_streams", "moe_aux_loss_seq",
            "moe_bias_update", "moe_route_expert_choice", "moe_expert_ffn_gather",
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
-           "moe_set_backward_streams"]
+           "moe_set_backward_streams", "NormConfig", "make_norm_config", "moe_block_norm",
+           "moe_block_norm_ws_bytes", "moe_block_norm_backward"]

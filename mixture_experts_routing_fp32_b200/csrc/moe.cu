@@ -1,6 +1,5 @@
-// libmoe.so: the extern "C" entry points declared in include/moe.h.
-// One translation unit (the device error word is a single __device__
-// variable); the kernels live in the .cuh files beside this one.
+// libmoe.so: the layer's extern "C" entry points declared in include/moe.h;
+// the kernels live in the .cuh files beside this one.  norm.cu holds the norms around the layer; what the units share is declared in host.cuh and defined at the end of this file.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -21,6 +20,7 @@
 #include "gemm_simt.cuh"
 #include "gemm_tc.cuh"
 #include "router_tc.cuh"
+#include "host.cuh"
 
 using namespace moe;
 
@@ -2154,3 +2154,24 @@ int64_t moe_launch_count(int reset) {
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// shared with the other translation units (host.cuh)
+// ---------------------------------------------------------------------------
+namespace moe {
+namespace host {
+
+int fail(cudaError_t e) {
+  g_last_cuda_error = (int)e;
+  return MOE_ERR_CUDA;
+}
+void before_launch(cudaStream_t s) { prof_begin(s); }
+int after_launch(cudaStream_t s, const char* name) {
+  MOE_LAUNCHED(s, name);
+  return MOE_OK;
+}
+bool use_pdl() { return pdl_enabled(); }
+int sm_count() { return num_sms(); }
+
+}  // namespace host
+}  // namespace moe

@@ -564,6 +564,70 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* r_out, con
                             float* db_post, float* dgate, float* dw_pre, float* db_pre,
                             void* ws, cudaStream_t stream);
 
+/*
+ * AdamW (decoupled weight decay) over a list of tensors.  With t the count of this step,
+ *   g  = grad * grad_scale
+ *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
+ *   p' = p - lr ((m'/(1-beta1^t)) / (sqrt(v'/(1-beta2^t)) + eps) + weight_decay p)
+ * in fp32.  Hyper-parameters are double so that 1 - beta keeps its digits.
+ */
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+} moe_adamw_config_t;
+
+enum { MOE_STATE_FP32 = 0, MOE_STATE_FP8 = 1 };  /* moe_adamw_tensor_t.state */
+#define MOE_ADAMW_BLOCK 256   /* consecutive elements that share a scale */
+
+/*
+ * One tensor of n consecutive elements.  Pointers are aligned to their
+ * element type; tensors whose pointers are 16-byte aligned run with wide
+ * accesses.
+ *   param   type `dtype` in/out; grad: type `grad_dtype`
+ *   master  [n] f32 in/out or NULL: the weight at full precision, from which
+ *           param (then only written) is rounded
+ *   m, v    MOE_STATE_FP32: [n] f32 in/out.  MOE_STATE_FP8: [n] e4m3 in/out,
+ *           scaled by blocks of MOE_ADAMW_BLOCK elements: m = m8 * m_scale[b],
+ *           sqrt(v) = v8 * v_scale[b] with the largest of the block at 448
+ *           (the root halves the range that 8 bits have to span; a positive
+ *           v never rounds to zero).  A block whose largest value is below
+ *           2^-100 holds zeros.  A NaN or infinity in grad makes its block's
+ *           states NaN.
+ *   m_scale, v_scale  [ceil(n / MOE_ADAMW_BLOCK)] f32 in/out (NULL for MOE_STATE_FP32)
+ *   lr_mult  multiplies lr; decay: 0 or 1, whether weight decay applies
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  int32_t dtype, grad_dtype;     /* MOE_FP32, MOE_BF16 */
+  int32_t state;
+  int32_t decay;
+  float lr_mult;
+  int32_t reserved;              /* 0 */
+} moe_adamw_tensor_t;
+
+/*
+ * moe_adamw — one optimizer step over n_tensors tensors (a HOST array, read
+ * during the call; the pointers in it are baked into a captured graph).
+ *   step        [2] i32 in/out, device: step[0] steps were taken before, the
+ *               call makes it one more; step[1] is the kernel's own and has
+ *               to be 0 before the first call
+ *   lr          [1] f32 device or NULL: the learning rate, in place of cfg's
+ *               (a schedule under graph replay)
+ *   grad_scale  [1] f32 device or NULL (1): a clipping or loss-scale factor
+ * Tensors of n = 0 are passed over; tensors must not overlap.  One launch
+ * for every MOE_ADAMW_MAX tensors.
+ */
+#define MOE_ADAMW_MAX 40
+int moe_adamw(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tensors,
+              int32_t n_tensors, int32_t* step, const float* lr, const float* grad_scale,
+              cudaStream_t stream);
+
 /* Synchronises `stream`, reads and clears the device error word (bits in
  * *bits if non-NULL).  MOE_OK, MOE_ERR_DEVICE or MOE_ERR_CUDA. */
 int moe_check_status(cudaStream_t stream, uint32_t* bits);

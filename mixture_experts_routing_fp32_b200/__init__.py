@@ -12,7 +12,9 @@ from .api import (MoEError, MoeConfig, MoeSizes, config_from, make_config,
                   moe_route_expert_choice, moe_expert_ffn_gather,
                   moe_expert_ffn_combine, moe_aux_stats, moe_aux_loss_global,
                   moe_set_backward_streams, NormConfig, make_norm_config, moe_block_norm,
-                  moe_block_norm_backward, moe_block_norm_ws_bytes)
+                  moe_block_norm_backward, moe_block_norm_ws_bytes, AdamwConfig, AdamwTable,
+                  adamw_table, make_adamw_config, moe_adamw)
+from .optim import MoEAdamW
 from .layer import MoELayer
 
 __all__ = ["MoEError", "MoeConfig", "MoeSizes", "config_from", "make_config",
@@ -22,4 +24,5 @@ __all__ = ["MoEError", "MoeConfig", "MoeSizes", "config_from", "make_config",
            "moe_route_expert_choice", "moe_expert_ffn_gather",
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
            "moe_set_backward_streams", "NormConfig", "make_norm_config", "moe_block_norm",
-           "moe_block_norm_backward", "moe_block_norm_ws_bytes", "MoELayer"]
+           "moe_block_norm_backward", "moe_block_norm_ws_bytes", "AdamwConfig", "AdamwTable",
+           "adamw_table", "make_adamw_config", "moe_adamw", "MoEAdamW", "MoELayer"]

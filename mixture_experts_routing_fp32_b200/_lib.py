@@ -18,6 +18,8 @@ MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 MOE_GMAX, MOE_GTOP2SUM = 0, 1
 MOE_GEMM_AUTO, MOE_GEMM_SIMT = 0, 1
 MOE_RMSNORM, MOE_LAYERNORM = 0, 1
+MOE_STATE_FP32, MOE_STATE_FP8 = 0, 1
+MOE_ADAMW_BLOCK = 256
 DEVERR_EXPERT_ID, DEVERR_TIMEOUT, DEVERR_ROWS = 1, 2, 4
 
 c_int32, c_int64, c_float, c_void_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
@@ -32,7 +34,8 @@ EXPORTS = ("moe_get_sizes", "moe_router", "moe_dispatch", "moe_aux_loss",
            "moe_bias_update", "moe_route_expert_choice", "moe_expert_ffn_gather",
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
            "moe_set_backward_streams",
-           "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_ws_bytes")
+           "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_ws_bytes",
+           "moe_adamw")
 
 
 class MoeConfig(ctypes.Structure):
@@ -57,6 +60,17 @@ class NormConfig(ctypes.Structure):
     _fields_ = [("T", c_int32), ("D", c_int32), ("norm", c_int32), ("dtype", c_int32),
                 ("resid", c_int32), ("gate_len", c_int32), ("eps", c_float),
                 ("alpha", c_float)]
+
+
+class AdamwConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("param", "grad", "master", "m", "v", "m_scale",
+                                        "v_scale")] + [
+        ("n", c_int64), ("dtype", c_int32), ("grad_dtype", c_int32), ("state", c_int32),
+        ("decay", c_int32), ("lr_mult", c_float), ("reserved", c_int32)]
 
 
 class MoEError(RuntimeError):
@@ -111,6 +125,8 @@ def lib():
         "moe_block_norm": [norm] + [P] * 11,
         "moe_block_norm_backward": [norm] + [P] * 18,
         "moe_block_norm_ws_bytes": [norm],
+        "moe_adamw": [ctypes.POINTER(AdamwConfig), ctypes.POINTER(AdamwTensor), c_int32, P, P,
+                      P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

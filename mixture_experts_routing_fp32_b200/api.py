@@ -10,7 +10,8 @@ import ctypes
 
 import torch
 
-from ._lib import MoeConfig, MoeSizes, MoEError, NormConfig, check, lib
+from ._lib import (AdamwConfig, AdamwTensor, MoeConfig, MoeSizes, MoEError, NormConfig, check,
+                   lib)
 from . import _lib as C
 
 
@@ -216,6 +217,64 @@ def moe_block_norm_backward(cfg, r_out, y, w_post, b_post, gate, w_pre, stats, d
         _p(dw_pre), _p(db_pre), _p(ws), _s(stream)), "moe_block_norm_backward")
 
 
+def make_adamw_config(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+                      weight_decay=0.01) -> AdamwConfig:
+    return AdamwConfig(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
+
+
+class AdamwTable:
+    """The tensors of an optimizer step, described once (it keeps them alive)."""
+
+    def __init__(self, array, count, device, tensors):
+        self.array, self.count, self.device, self.tensors = array, count, device, tensors
+
+
+def adamw_table(entries) -> AdamwTable:
+    """Describes the tensors of an AdamW step.  Each entry is a mapping with
+    `param`, `grad`, `m`, `v` (contiguous CUDA tensors of the same length;
+    m and v fp32, or float8_e4m3fn with `m_scale` and `v_scale`, fp32 with
+    one element per 256) and, if wanted, `master` (fp32), `lr_mult` (1.0)
+    and `decay` (True)."""
+    types = {torch.float32: C.MOE_FP32, torch.bfloat16: C.MOE_BF16}
+    entries = [dict(e) for e in entries]
+    arr = (AdamwTensor * max(1, len(entries)))()
+    device = None
+    for a, e in zip(arr, entries):
+        p, m = e["param"], e["m"]
+        n, fp8 = p.numel(), m.dtype == torch.float8_e4m3fn
+        nb = -(-n // C.MOE_ADAMW_BLOCK)
+        scale = (torch.float32, nb) if fp8 else (None, 0)
+        state = (m.dtype if fp8 else torch.float32, n)
+        wants = {"param": (p.dtype, n), "grad": (e["grad"].dtype, n), "m": state, "v": state,
+                 "master": (torch.float32, n), "m_scale": scale, "v_scale": scale}
+        for k, (dt, count) in wants.items():
+            t = e.get(k)
+            if t is None:
+                if k == "master" or (k.endswith("_scale") and not fp8):
+                    continue
+                raise MoEError("adamw_table: %s is missing" % k)
+            if k in ("param", "grad") and t.dtype not in types:
+                raise MoEError("adamw_table: %s is fp32 or bf16, not %s" % (k, t.dtype))
+            if t.dtype != dt or t.numel() != count or not t.is_contiguous() or not t.is_cuda:
+                raise MoEError("adamw_table: %s is not a contiguous CUDA tensor of %d x %s"
+                               % (k, count, dt))
+            device = t.device if device is None else device
+            if t.device != device:
+                raise MoEError("adamw_table: tensors on %s and %s" % (device, t.device))
+            setattr(a, k, t.data_ptr())
+        a.n, a.dtype, a.grad_dtype = n, types[p.dtype], types[e["grad"].dtype]
+        a.state = C.MOE_STATE_FP8 if fp8 else C.MOE_STATE_FP32
+        a.decay, a.lr_mult, a.reserved = int(bool(e.get("decay", True))), e.get("lr_mult", 1.0), 0
+    return AdamwTable(arr, len(entries), device, entries)
+
+
+def moe_adamw(cfg, table, step, lr=None, grad_scale=None, stream=None):
+    """One AdamW step over an adamw_table; step: int32 [2] device tensor (the
+    count of steps taken, and a word of the kernel's own that starts at 0)."""
+    check(lib().moe_adamw(ctypes.byref(cfg), table.array, table.count, _p(step), _p(lr),
+                          _p(grad_scale), _s(stream)), "moe_adamw")
+
+
 def moe_check_status(stream=None) -> int:
     bits = ctypes.c_uint32(0)
     rc = lib().moe_check_status(_s(stream), ctypes.byref(bits))
@@ -274,4 +333,5 @@ __all__ = ["LaunchProfile", "MoEError", "MoeConfig", "MoeSizes", "make_config", 
            "moe_bias_update", "moe_route_expert_choice", "moe_expert_ffn_gather",
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
            "moe_set_backward_streams", "NormConfig", "make_norm_config", "moe_block_norm",
-           "moe_block_norm_ws_bytes", "moe_block_norm_backward"]
+           "moe_block_norm_ws_bytes", "moe_block_norm_backward", "AdamwConfig", "AdamwTable",
+           "make_adamw_config", "adamw_table", "moe_adamw"]

@@ -1,5 +1,6 @@
 // libmoe.so: the layer's extern "C" entry points declared in include/moe.h;
-// the kernels live in the .cuh files beside this one.  norm.cu holds the norms around the layer; what the units share is declared in host.cuh and defined at the end of this file.
+// the kernels live in the .cuh files beside this one.  norm.cu holds the norms
+// around the layer, adamw.cu the optimizer step; what the units share is declared in host.cuh and defined at the end of this file.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>

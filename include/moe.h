@@ -628,6 +628,52 @@ int moe_adamw(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tensors,
               int32_t n_tensors, int32_t* step, const float* lr, const float* grad_scale,
               cudaStream_t stream);
 
+/*
+ * moe_quant_i8 — symmetric 8-bit rows: scale[i] = max_j |x[i,j]| / 127,
+ * q[i,j] = round(127 x[i,j] / max_j |x[i,j]|) (ties to even; a row of zeros: q = 0).
+ * For weights [.., N, K] a row is a channel, for activations a token.
+ *   x      [rows] rows of cols elements, ld_x elements apart, type dtype
+ *   q      [rows, cols] i8 out;  scale [rows] f32 out
+ * A row with a NaN or an infinity gets scale NaN and q = 0.
+ * rows >= 0, 8 <= cols <= 65536, cols % 8 == 0, ld_x >= cols, ld_x % 8 == 0; x 16-byte and q 8-byte aligned.
+ */
+int moe_quant_i8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                 int8_t* q, float* scale, cudaStream_t stream);
+
+/* Workspace of moe_expert_ffn_i8 (256-byte aligned base).  Host-only; 0 for
+ * a cfg that moe_expert_ffn_i8 refuses. */
+int64_t moe_expert_ffn_i8_ws_bytes(const moe_config_t* cfg);
+
+/*
+ * moe_expert_ffn_i8 — the grouped SwiGLU experts in 8-bit integers, with a
+ * scale for each token and each output channel: the serving form of
+ * moe_expert_ffn (no activations are kept for a backward pass).  With
+ * q(v), s(v) as moe_quant_i8 gives them for a row v,
+ *   [a | b] = s(x) (q(x) w13^T) w13_scale,   h = silu(a) b   (fp32),
+ *   o       = s(h) (q(h) w_down^T) w_down_scale
+ * the products in integers (exact).  [STA324 §8.1, §8.8]
+ *   x          [T,D] act: layer input; each token is quantised once and
+ *              its 8-bit row goes to the rows of its slots
+ *   offsets, slot_row, row_slot, tile_expert, stats: moe_dispatch outputs
+ *              (x_perm is not needed: dispatch the layout only)
+ *   w13        [E,2F,D] i8, w13_scale [E,2F] f32: gate rows, then up rows
+ *   w_down     [E,D,F] i8,  w_down_scale [E,D] f32
+ *   w13_s, w13_s_scale, w_down_s, w_down_s_scale: the shared expert's
+ *              [2F,D], [2F], [D,F], [D] (NULL if n_shared = 0)
+ *   o          [rows_max,D] act out: expert outputs, for moe_combine
+ *   ws         workspace; calls that overlap need one each
+ * bf16 token-choice layers with D and F multiples of 128, at most 65536
+ * (MOE_ERR_ARG otherwise).  Expert shards (n_local_experts) hold their own
+ * experts' weights.  A token with a NaN or an infinity gets NaN rows of o,
+ * other tokens are not touched by it.
+ */
+int moe_expert_ffn_i8(const moe_config_t* cfg, const void* x, const int32_t* offsets,
+                      const int32_t* slot_row, const int32_t* row_slot,
+                      const int32_t* tile_expert, const int32_t* stats, const int8_t* w13,
+                      const float* w13_scale, const int8_t* w_down, const float* w_down_scale,
+                      const int8_t* w13_s, const float* w13_s_scale, const int8_t* w_down_s,
+                      const float* w_down_s_scale, void* o, void* ws, cudaStream_t stream);
+
 /* Synchronises `stream`, reads and clears the device error word (bits in
  * *bits if non-NULL).  MOE_OK, MOE_ERR_DEVICE or MOE_ERR_CUDA. */
 int moe_check_status(cudaStream_t stream, uint32_t* bits);

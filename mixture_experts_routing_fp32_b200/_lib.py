@@ -35,7 +35,7 @@ EXPORTS = ("moe_get_sizes", "moe_router", "moe_dispatch", "moe_aux_loss",
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
            "moe_set_backward_streams",
            "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_ws_bytes",
-           "moe_adamw")
+           "moe_adamw", "moe_quant_i8", "moe_expert_ffn_i8", "moe_expert_ffn_i8_ws_bytes")
 
 
 class MoeConfig(ctypes.Structure):
@@ -127,6 +127,9 @@ def lib():
         "moe_block_norm_ws_bytes": [norm],
         "moe_adamw": [ctypes.POINTER(AdamwConfig), ctypes.POINTER(AdamwTensor), c_int32, P, P,
                       P, P],
+        "moe_quant_i8": [P, c_int32, c_int64, c_int64, c_int64, P, P, P],
+        "moe_expert_ffn_i8": [cfg] + [P] * 17,
+        "moe_expert_ffn_i8_ws_bytes": [cfg],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -136,6 +139,7 @@ def lib():
     L.moe_launch_count.restype = ctypes.c_int64
     L.moe_profile_name.restype = ctypes.c_char_p
     L.moe_block_norm_ws_bytes.restype = ctypes.c_int64
+    L.moe_expert_ffn_i8_ws_bytes.restype = ctypes.c_int64
     _lib = L
     return L
 

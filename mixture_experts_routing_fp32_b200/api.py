@@ -275,6 +275,45 @@ def moe_adamw(cfg, table, step, lr=None, grad_scale=None, stream=None):
                           _p(grad_scale), _s(stream)), "moe_adamw")
 
 
+def moe_quant_i8(x, q, scale, stream=None):
+    """Rows of x (the last dimension; fp32 or bf16) to 8 bits with a scale
+    each.  x may be a row-strided matrix; more dimensions are contiguous."""
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    if x.dim() == 2 and x.stride(1) == 1:
+        ld = x.stride(0) if rows > 1 else cols
+    elif x.is_contiguous():
+        ld = cols
+    else:
+        raise MoEError("moe_quant_i8: x is not made of contiguous rows")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise MoEError("moe_quant_i8: x is fp32 or bf16, not %s" % x.dtype)
+    if (q.dtype != torch.int8 or q.shape != x.shape or not q.is_contiguous()
+            or scale.dtype != torch.float32 or scale.shape != x.shape[:-1]
+            or not scale.is_contiguous()):
+        raise MoEError("moe_quant_i8: q is int8 like x, scale fp32 with a value per row")
+    check(lib().moe_quant_i8(_p(x), _dtype(x.dtype), rows, cols, ld, _p(q), _p(scale),
+                             _s(stream)), "moe_quant_i8")
+
+
+def moe_expert_ffn_i8_ws_bytes(cfg) -> int:
+    """Workspace of moe_expert_ffn_i8."""
+    n = int(lib().moe_expert_ffn_i8_ws_bytes(ctypes.byref(cfg)))
+    if n <= 0:
+        check(C.MOE_ERR_ARG, "moe_expert_ffn_i8_ws_bytes")
+    return n
+
+
+def moe_expert_ffn_i8(cfg, x, offsets, slot_row, row_slot, tile_expert, stats, w13, w13_scale,
+                      w_down, w_down_scale, w13_s, w13_s_scale, w_down_s, w_down_s_scale, o, ws,
+                      stream=None):
+    check(lib().moe_expert_ffn_i8(
+        ctypes.byref(cfg), _p(x), _p(offsets), _p(slot_row), _p(row_slot), _p(tile_expert),
+        _p(stats), _p(w13), _p(w13_scale), _p(w_down), _p(w_down_scale), _p(w13_s),
+        _p(w13_s_scale), _p(w_down_s), _p(w_down_s_scale), _p(o), _p(ws), _s(stream)),
+        "moe_expert_ffn_i8")
+
+
 def moe_check_status(stream=None) -> int:
     bits = ctypes.c_uint32(0)
     rc = lib().moe_check_status(_s(stream), ctypes.byref(bits))
@@ -334,4 +373,5 @@ __all__ = ["LaunchProfile", "MoEError", "MoeConfig", "MoeSizes", "make_config", 
            "moe_expert_ffn_combine", "moe_aux_stats", "moe_aux_loss_global",
            "moe_set_backward_streams", "NormConfig", "make_norm_config", "moe_block_norm",
            "moe_block_norm_ws_bytes", "moe_block_norm_backward", "AdamwConfig", "AdamwTable",
-           "make_adamw_config", "adamw_table", "moe_adamw"]
+           "make_adamw_config", "adamw_table", "moe_adamw", "moe_quant_i8",
+           "moe_expert_ffn_i8", "moe_expert_ffn_i8_ws_bytes"]

@@ -1,0 +1,400 @@
+// The experts in 8-bit integers: row quantisation, the quantised dispatch of
+// tokens, the two grouped products (gemm_i8.cuh) and the requantisation of h
+// between them.
+//
+//   q(v)_j = round(127 v_j / max|v|),  s(v) = max|v| / 127   for a row v
+//
+// The quotient is formed as a division of 127 v_j (exact for bf16 v_j), so a
+// tie of the definition is a tie here and goes to even.
+#include "host.cuh"
+#include "gemm_i8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr int kMaxCols = 65536;
+
+// Power of two that keeps 127 v and the quotient's parts in range whatever
+// the row's magnitude (exact, so the quotient does not change).
+__device__ __forceinline__ float range_shift(float big) {
+  return big < 7.9e-31f ? 1.8446744e19f : big > 1e36f ? 9.765625e-4f : 1.0f;   // 2^64, 2^-10
+}
+__device__ __forceinline__ int quantised(float v, float shift, float big) {
+  return __float2int_rn(127.0f * (v * shift) / big);
+}
+__device__ __forceinline__ uint2 pack8_i8(const int* q) {
+  uint2 u;
+  u.x = (q[0] & 255) | ((q[1] & 255) << 8) | ((q[2] & 255) << 16) | ((uint32_t)q[3] << 24);
+  u.y = (q[4] & 255) | ((q[5] & 255) << 8) | ((q[6] & 255) << 16) | ((uint32_t)q[7] << 24);
+  return u;
+}
+// Largest magnitude's bits over a block (NaN orders above infinity).
+__device__ __forceinline__ unsigned block_max(unsigned v, unsigned* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();            // the previous row's readers are done
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = lane < (kQThreads >> 5) ? red[lane] : 0u;
+  return __reduce_max_sync(0xffffffffu, v);
+}
+__device__ __forceinline__ unsigned max_bits(const float* f, unsigned m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+  return m;
+}
+
+// One row per block and turn, NV pieces of 8 columns per thread held in
+// registers between the maximum and the rounding; NV = 0: rows longer than
+// that are read twice (the second time from L2).  out(col, packed) stores 8
+// values; the scale is returned.
+template <typename TX, int NV, typename Out>
+__device__ __forceinline__ float quantise_row(const TX* x, int cols, unsigned* red, Out out) {
+  const int nv = cols / 8;
+  unsigned m = 0;
+  Raw8<TX> keep[NV > 0 ? NV : 1];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = threadIdx.x + i * kQThreads;
+      if (c < nv) keep[i].load(x + 8 * (int64_t)c);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[8];
+      keep[i].widen(f);
+      if (threadIdx.x + i * kQThreads < nv) m = max_bits(f, m);
+    }
+  } else {
+    for (int c = threadIdx.x; c < nv; c += kQThreads) {
+      float f[8];
+      load8(x + 8 * (int64_t)c, f);
+      m = max_bits(f, m);
+    }
+  }
+  m = block_max(m, red);
+  const bool finite = m < 0x7f800000u;
+  const float big = __uint_as_float(m);
+  const float shift = range_shift(big), den = big > 0.f ? big * shift : 1.0f;
+  auto put = [&](const float* f, int c) {
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = finite ? quantised(f[i], shift, den) : 0;
+    out(8 * c, pack8_i8(q));
+  };
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = threadIdx.x + i * kQThreads;
+      float f[8];
+      keep[i].widen(f);
+      if (c < nv) put(f, c);
+    }
+  } else {
+    for (int c = threadIdx.x; c < nv; c += kQThreads) {
+      float f[8];
+      load8(x + 8 * (int64_t)c, f);
+      put(f, c);
+    }
+  }
+  return i8::scale_of(m);
+}
+
+template <typename TX, int NV>
+__global__ void __launch_bounds__(kQThreads)
+quant_rows_kernel(const TX* x, int64_t rows, int cols, int64_t ld, int8_t* q, float* scale) {
+  __shared__ unsigned red[32];
+  pdl_begin();
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    int8_t* dst = q + r * cols;
+    const float s = quantise_row<TX, NV>(x + r * ld, cols, red, [&](int c, uint2 u) {
+      *reinterpret_cast<uint2*>(dst + c) = u;
+    });
+    if (threadIdx.x == 0) scale[r] = s;
+  }
+}
+
+// Tokens: each row of x is read and quantised once and its 8-bit form goes
+// to every row that holds the token (its slots' rows, the shared expert's).
+// The blocks behind the last token count the rows in use of each 128-row
+// tile: a routed expert's rows are a prefix of its segment, so the tile's
+// count is that of its non-negative row slots.
+template <int NV>
+__global__ void __launch_bounds__(kQThreads)
+quant_dispatch_kernel(const __nv_bfloat16* x, int T, int D, int K, int E, int n_shared,
+                      const int32_t* offsets, const int32_t* slot_row, const int32_t* row_slot,
+                      const int32_t* stats, int token_blocks, int8_t* xq, float* scale,
+                      unsigned* row_max, int32_t* tile_rows) {
+  __shared__ unsigned red[32];
+  pdl_begin();
+  if ((int)blockIdx.x >= token_blocks) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_tiles = stats[3], shared0 = offsets[E] / kRowTile;
+    const int step = (gridDim.x - token_blocks) * (kQThreads >> 5);
+    for (int t = (blockIdx.x - token_blocks) * (kQThreads >> 5) + warp; t < n_tiles; t += step) {
+      int n = 0;
+      if (t >= shared0) {
+        n = max(0, min(kRowTile, T - (t - shared0) * kRowTile));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRowTile / 32; ++i)
+          n += __popc(__ballot_sync(0xffffffffu, row_slot[t * kRowTile + i * 32 + lane] >= 0));
+      }
+      if (lane == 0) tile_rows[t] = n;
+    }
+    return;
+  }
+  const int shared_row = n_shared ? offsets[E] : -1;
+  for (int t = blockIdx.x; t < T; t += token_blocks) {
+    const int32_t* rows = slot_row + (int64_t)t * K;
+    const float s = quantise_row<__nv_bfloat16, NV>(
+        x + (int64_t)t * D, D, red, [&](int c, uint2 u) {
+          for (int k = 0; k < K; ++k) {
+            const int r = rows[k];
+            if (r >= 0) *reinterpret_cast<uint2*>(xq + (int64_t)r * D + c) = u;
+          }
+          if (shared_row >= 0)
+            *reinterpret_cast<uint2*>(xq + (int64_t)(shared_row + t) * D + c) = u;
+        });
+    for (int k = threadIdx.x; k <= K; k += kQThreads) {
+      const int r = k < K ? rows[k] : shared_row >= 0 ? shared_row + t : -1;
+      if (r >= 0) {
+        scale[r] = s;
+        row_max[r] = 0u;
+      }
+    }
+  }
+}
+
+// h (fp32, each row's largest magnitude already known from the product's
+// epilogue) to 8 bits: 16 columns a thread, 512 a warp and turn.  h is fp32,
+// where ties mean nothing, so the quotient is a product with 127 / max.
+__global__ void __launch_bounds__(kQThreads)
+quant_h_kernel(const float* h, int F, const int32_t* stats, const int32_t* tile_rows,
+               const unsigned* row_max, int8_t* hq) {
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int per = (F + 511) / 512;
+  const int64_t total = (int64_t)stats[2] * per;
+  const int64_t step = (int64_t)gridDim.x * (kQThreads >> 5);
+  for (int64_t u = (int64_t)blockIdx.x * (kQThreads >> 5) + (threadIdx.x >> 5); u < total;
+       u += step) {
+    const int64_t r = u / per;
+    const int c = (int)(u - r * per) * 512 + lane * 16;
+    if (c >= F || (int)(r % kRowTile) >= tile_rows[r / kRowTile]) continue;
+    const unsigned bits = row_max[r];
+    const float big = __uint_as_float(bits);
+    const float shift = range_shift(big);
+    const float inv = (bits < 0x7f800000u && bits > 0u) ? 127.0f / (big * shift) : 0.f;
+    float f[16];
+    load8(h + r * F + c, f);
+    load8(h + r * F + c + 8, f + 8);
+    int q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q[i] = inv > 0.f ? __float2int_rn(f[i] * shift * inv) : 0;
+    const uint2 a = pack8_i8(q), b = pack8_i8(q + 8);
+    *reinterpret_cast<uint4*>(hq + r * F + c) = make_uint4(a.x, a.y, b.x, b.y);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+struct Work {
+  host::LayerView v;
+  int64_t xq, xs, h, hq, row_max, tile_rows, total;
+};
+constexpr int64_t kAlign = 256;
+
+int work_of(const moe_config_t* c, Work* w) {
+  MOE_HTRY(host::layer_view(c, &w->v));
+  // (sums of 65536 products of 8-bit values stay below 2^31)
+  if (!w->v.tensor_cores || c->expert_choice || c->D > kMaxCols || c->F > kMaxCols)
+    return MOE_ERR_ARG;
+  int64_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = off;
+    off += host::ceil_div(bytes, kAlign) * kAlign;
+    return at;
+  };
+  const int64_t R = w->v.rows_max;
+  w->xq = take(R * c->D);
+  w->xs = take(R * 4);
+  w->h = take(R * c->F * 4);
+  w->hq = take(R * c->F);
+  w->row_max = take(R * 4);
+  w->tile_rows = take(w->v.tiles_max * 4);
+  w->total = off;
+  return MOE_OK;
+}
+
+template <int BN, int ST, int EPI, bool PAIR>
+int run_gemm(const char* name, const CUtensorMap& a, const CUtensorMap& a16, const CUtensorMap& b,
+             const CUtensorMap& bs, const CUtensorMap& o, const i8::Params& p, int64_t units,
+             cudaStream_t s) {
+  using S = i8::Smem<BN, ST, PAIR>;
+  auto k = i8::gemm_i8_kernel<BN, ST, EPI, PAIR>;
+  MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes));
+  const int64_t items = units * p.nN;
+  if (items <= 0) return MOE_OK;
+  int64_t resident = host::sm_count();
+  if (PAIR) MOE_HTRY(host::resident_clusters(k, 2, tc::kThreads, S::kBytes, &resident));
+  const int ctas = (int)std::min<int64_t>(resident, items) * (PAIR ? 2 : 1);
+  return host::launch(name, k, ctas, tc::kThreads, S::kBytes, s, PAIR ? 2 : 1, a, a16, b, bs, o, p);
+}
+
+// Row tiles per rasterisation group: as many row tiles of depth K bytes as
+// fit in about 24 MiB of L2.
+int group_rows(int64_t k_bytes, bool pair) {
+  const int64_t rows = pair ? 256 : 128;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(64, (24ll << 20) / (rows * k_bytes)));
+}
+
+template <int EPI>
+int product(const moe_config_t* c, const Work& w, const char* name, const int8_t* a, int64_t K,
+            const int8_t* b, const int8_t* b_s, int64_t cols, void* out, i8::Params p,
+            cudaStream_t s) {
+  const bool pair = w.v.align == 256;
+  const int64_t n_out = EPI == i8::I8_SWIGLU ? c->F : c->D;
+  // tiles that run at once: few row tiles (decoding) take narrow column
+  // tiles, so that every SM streams weights
+  const int64_t slots = (int64_t)c->T * c->K;
+  const int64_t mt = std::min<int64_t>(w.v.tiles_max,
+                                       std::min<int64_t>(w.v.local_experts, slots) +
+                                           slots / kRowTile + (c->n_shared ? host::ceil_div(c->T, 128) : 0));
+  const int sms = host::sm_count();
+  int bn = 256;
+  if (!pair) {
+    const int64_t tiles256 = mt * host::ceil_div(n_out, EPI == i8::I8_SWIGLU ? 128 : 256);
+    if (tiles256 < 2 * sms) bn = 128;
+    if (EPI == i8::I8_STORE && mt * host::ceil_div(n_out, 128) < 2 * sms) bn = 64;
+  }
+  // D and F are multiples of 128: a 256-wide plain tile may not divide D
+  if (EPI == i8::I8_STORE && n_out % bn) bn = 128;
+  const int tile_n = EPI == i8::I8_SWIGLU ? bn / 2 : bn;
+  p.E = w.v.local_experts; p.F = c->F; p.nk = (int)(K / i8::kBK); p.nN = (int)(n_out / tile_n);
+  p.group_m = group_rows(K, pair); p.cols = (int)cols;
+  CUtensorMap ma, ma16, mb, mbs, mo;
+  MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, K, 128));
+  MOE_HTRY(host::make_map_u8(&ma16, a, 1, w.v.rows_max, K, 16));
+  const uint32_t box = (uint32_t)(EPI == i8::I8_SWIGLU || pair ? bn / 2 : bn);
+  MOE_HTRY(host::make_map_u8(&mb, b, w.v.local_experts, cols, K, box));
+  MOE_HTRY(host::make_map_u8(&mbs, b_s != nullptr ? b_s : b, 1, cols, K, box));
+  MOE_HTRY(host::make_out_map(&mo, out, w.v.rows_max, n_out, EPI == i8::I8_SWIGLU));
+  const int64_t units = w.v.tiles_max / (pair ? 2 : 1);
+  if (pair) {
+    if (bn == 256) return run_gemm<256, 5, EPI, true>(name, ma, ma16, mb, mbs, mo, p, units, s);
+    return run_gemm<128, 6, EPI, true>(name, ma, ma16, mb, mbs, mo, p, units, s);
+  }
+  if (bn == 256) return run_gemm<256, 4, EPI, false>(name, ma, ma16, mb, mbs, mo, p, units, s);
+  if constexpr (EPI == i8::I8_STORE) {
+    if (bn == 64) return run_gemm<64, 7, EPI, false>(name, ma, ma16, mb, mbs, mo, p, units, s);
+  }
+  return run_gemm<128, 5, EPI, false>(name, ma, ma16, mb, mbs, mo, p, units, s);
+}
+
+template <typename TX>
+int quant_rows(const TX* x, int64_t rows, int64_t cols, int64_t ld, int8_t* q, float* scale,
+               cudaStream_t s) {
+  const int grid = (int)std::min<int64_t>(rows, (int64_t)host::sm_count() * 8);
+  const int64_t nv = host::ceil_div(cols / 8, kQThreads);
+  auto go = [&](auto k) {
+    return host::launch("quant_i8", k, grid, kQThreads, 0, s, 1, x, rows, (int)cols, ld, q, scale);
+  };
+  if (nv <= 1) return go(quant_rows_kernel<TX, 1>);
+  if (nv <= 2) return go(quant_rows_kernel<TX, 2>);
+  if (nv <= 4) return go(quant_rows_kernel<TX, 4>);
+  return go(quant_rows_kernel<TX, 0>);
+}
+
+}  // namespace
+
+namespace host {
+int take_i8_error(unsigned* bits) {
+  unsigned zero = 0;
+  MOE_HCK(cudaMemcpyFromSymbol(bits, g_dev_error, sizeof(*bits)));
+  if (*bits) MOE_HCK(cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero)));
+  return MOE_OK;
+}
+}  // namespace host
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_quant_i8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                 int8_t* q, float* scale, cudaStream_t s) {
+  if (dtype != MOE_FP32 && dtype != MOE_BF16) return MOE_ERR_ARG;
+  if (rows < 0 || cols < 8 || cols > kMaxCols || cols % 8 || ld_x < cols || ld_x % 8)
+    return MOE_ERR_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scale || host::misaligned(x, 16) || host::misaligned(q, 8) ||
+      host::misaligned(scale, 4))
+    return MOE_ERR_ARG;
+  if (dtype == MOE_BF16)
+    return quant_rows(static_cast<const __nv_bfloat16*>(x), rows, cols, ld_x, q, scale, s);
+  return quant_rows(static_cast<const float*>(x), rows, cols, ld_x, q, scale, s);
+}
+
+int64_t moe_expert_ffn_i8_ws_bytes(const moe_config_t* c) {
+  Work w;
+  return work_of(c, &w) == MOE_OK ? w.total : 0;
+}
+
+int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offsets,
+                      const int32_t* slot_row, const int32_t* row_slot,
+                      const int32_t* tile_expert, const int32_t* stats, const int8_t* w13,
+                      const float* w13_scale, const int8_t* w_down, const float* w_down_scale,
+                      const int8_t* w13_s, const float* w13_s_scale, const int8_t* w_down_s,
+                      const float* w_down_s_scale, void* o, void* ws, cudaStream_t s) {
+  Work w;
+  MOE_HTRY(work_of(c, &w));
+  if (!x || !offsets || !slot_row || !row_slot || !tile_expert || !stats || !w13 || !w13_scale ||
+      !w_down || !w_down_scale || !o || !ws)
+    return MOE_ERR_ARG;
+  if (c->n_shared && (!w13_s || !w13_s_scale || !w_down_s || !w_down_s_scale)) return MOE_ERR_ARG;
+  for (const void* p : {x, (const void*)w13, (const void*)w13_scale, (const void*)w_down,
+                        (const void*)w_down_scale, (const void*)w13_s, (const void*)w13_s_scale,
+                        (const void*)w_down_s, (const void*)w_down_s_scale, (const void*)o})
+    if (host::misaligned(p, 16)) return MOE_ERR_ARG;
+  if (host::misaligned(ws, kAlign)) return MOE_ERR_ARG;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int8_t* xq = reinterpret_cast<int8_t*>(base + w.xq);
+  int8_t* hq = reinterpret_cast<int8_t*>(base + w.hq);
+  float* xs = reinterpret_cast<float*>(base + w.xs);
+  float* h = reinterpret_cast<float*>(base + w.h);
+  unsigned* row_max = reinterpret_cast<unsigned*>(base + w.row_max);
+  int32_t* tile_rows = reinterpret_cast<int32_t*>(base + w.tile_rows);
+  const int sms = host::sm_count();
+  {
+    const int tokens = (int)std::min<int64_t>(c->T, (int64_t)sms * 8);
+    const int tiles = (int)std::min<int64_t>(host::ceil_div(w.v.tiles_max, kQThreads / 32), 64);
+    auto go = [&](auto k) {
+      return host::launch("quant_dispatch", k, tokens + tiles, kQThreads, 0, s, 1,
+                          static_cast<const __nv_bfloat16*>(x), c->T, c->D, c->K,
+                          w.v.local_experts, c->n_shared, offsets, slot_row, row_slot, stats,
+                          tokens, xq, xs, row_max, tile_rows);
+    };
+    const int64_t nv = host::ceil_div(c->D / 8, kQThreads);
+    if (nv <= 1) MOE_HTRY(go(quant_dispatch_kernel<1>));
+    else if (nv <= 2) MOE_HTRY(go(quant_dispatch_kernel<2>));
+    else if (nv <= 4) MOE_HTRY(go(quant_dispatch_kernel<4>));
+    else MOE_HTRY(go(quant_dispatch_kernel<0>));
+  }
+  i8::Params p{};
+  p.tile_expert = tile_expert; p.tile_rows = tile_rows; p.stats = stats;
+  p.row_scale = xs; p.row_max = row_max;
+  p.col_scale = w13_scale; p.col_scale_s = w13_s_scale;
+  MOE_HTRY((product<i8::I8_SWIGLU>(c, w, "i8_gate_up", xq, c->D, w13, w13_s, 2 * (int64_t)c->F, h,
+                                   p, s)));
+  MOE_HTRY(host::launch("quant_h", quant_h_kernel,
+                        (int)std::min<int64_t>(host::ceil_div(w.v.rows_max * host::ceil_div(c->F, 512), 8),
+                                               (int64_t)sms * 8),
+                        kQThreads, 0, s, 1, h, c->F, stats, tile_rows, row_max, hq));
+  p.col_scale = w_down_scale; p.col_scale_s = w_down_s_scale;
+  return product<i8::I8_STORE>(c, w, "i8_down", hq, c->F, w_down, w_down_s, c->D, o, p, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,428 @@
+// Grouped tensor-core products in 8-bit integers (tcgen05 kind::i8) with a
+// scale for each row (token) and each column (output channel):
+//
+//   C[r, n] = s_r t_{e,n} sum_k A[r, k] B_e[n, k]       (sums in int32, exact)
+//
+// over the permuted rows of the dispatch, for the two products of the SwiGLU
+// experts: gate/up (the epilogue forms h = silu(a) b in fp32, writes it and
+// keeps each row's largest |h|) and down (bf16 out).
+//
+// The kernel is the bf16 grouped product's in outline: persistent CTAs (or
+// CTA pairs sharing 256-row MMAs), a TMA producer warp filling a ring of
+// 128-byte-swizzled stages, one thread issuing MMAs (K = 32) into a ring of
+// accumulators in tensor memory, eight epilogue warps.  In bytes a stage is
+// the bf16 kernel's (128 bytes of k per row, now 128 elements), and every
+// MMA does twice the products on them, so the operands' way into the SM
+// bounds it sooner.  Tiles of few rows (decoding) load only the 16-row
+// pieces of A that hold tokens: the rest of the stage keeps whatever integers
+// it held, whose products land in accumulator rows that nothing stores.
+#pragma once
+#include "gemm_tc.cuh"
+
+namespace moe {
+namespace i8 {
+
+using namespace tc;
+
+constexpr int kBK = 128;          // k per stage: one 128-byte swizzle row
+constexpr int kUmmaK = 32;        // k of one 8-bit MMA
+enum { I8_SWIGLU = 0, I8_STORE = 1 };
+
+struct Params {
+  int E, F, nk, nN, group_m;
+  const int32_t* tile_expert;
+  const int32_t* tile_rows;       // rows in use of each 128-row tile
+  const int32_t* stats;           // stats[3]: 128-row tiles in use
+  const float* row_scale;         // I8_SWIGLU: s_r
+  unsigned* row_max;              // I8_SWIGLU out / I8_STORE in: bits of max |h| of each row
+  const float* col_scale;         // [E, cols]
+  const float* col_scale_s;       // shared expert
+  int cols;                       // 2F or D
+};
+
+__device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void umma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+// Instruction descriptor: kind::i8, s8 x s8 -> s32, both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void tma_3d_pair_hint(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar, int c0, int c1, int c2,
+                                                 uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(pol)
+      : "memory");
+}
+
+// Scale of a row from the bits of its largest |h|; NaN when that is not
+// finite (its 8-bit values are zeros then).
+__device__ __forceinline__ float scale_of(unsigned bits) {
+  return bits >= 0x7f800000u ? __int_as_float(0x7fffffff) : __uint_as_float(bits) / 127.0f;
+}
+
+template <int BN, int STAGES, bool PAIR>
+struct Smem {
+  static constexpr int BNC = PAIR ? BN / 2 : BN;      // columns of B this CTA holds
+  static constexpr int NACC = BN <= 128 ? 4 : BN <= 256 ? 2 : 1;
+  static constexpr int kA = BM * kBK;
+  static constexpr int kB = BNC * kBK;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kBars = (2 * STAGES + 2 * NACC + 1) * 8;
+  static constexpr int kEpiOff = (STAGES * kStage + kBars + 16 + 1023) / 1024 * 1024;
+  static constexpr int kStgW = 4096;                  // one 32 x 32 fp32 box, or two bf16 boxes
+  static constexpr int kBytes = 1024 + kEpiOff + kEpiWarps * kStgW;
+  static_assert(kBytes <= 232448 - 64, "shared memory per CTA");
+};
+
+struct Tile8 {
+  int e, m0, n0, rows;
+};
+
+template <int EPI, int BN, bool PAIR>
+__device__ __forceinline__ Tile8 decode8(int t, const Params& p, int rank, int n_mt) {
+  constexpr int MU = PAIR ? 2 * BM : BM;
+  const int group = t / (p.group_m * p.nN);
+  const int first = group * p.group_m;
+  const int gm = min(p.group_m, n_mt - first);
+  const int local = t - group * p.group_m * p.nN;
+  const int mt = first + local % gm, nt = local / gm;
+  Tile8 d;
+  d.e = p.tile_expert[mt * (MU / BM)];
+  d.m0 = mt * MU + rank * BM;
+  d.n0 = nt * (EPI == I8_SWIGLU ? BN / 2 : BN);
+  d.rows = p.tile_rows[mt * (MU / BM) + rank];
+  return d;
+}
+
+// mapA: [rows_max][K] in 128-row boxes, mapA16: the same in 16-row boxes;
+// mapB / mapBs: [E][cols][K] (the shared expert's own); mapO: h [rows_max][F]
+// fp32, or o [rows_max][D] bf16, for the epilogue's TMA stores.
+template <int BN, int STAGES, int EPI, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapA16,
+               const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapBs,
+               const __grid_constant__ CUtensorMap mapO, const Params p) {
+  using S = Smem<BN, STAGES, PAIR>;
+  constexpr int NACC = S::NACC;
+  constexpr int NBM = BN > 256 ? BN / 256 : 1;       // MMAs per k step (N at most 256 each)
+  constexpr int NMM = BN / NBM;
+  constexpr int BLK = PAIR ? NMM / 2 : NMM;          // B rows per CTA and MMA
+  static_assert(BN <= 256 || PAIR, "512-wide tiles only on CTA pairs");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int abort_flag_s;
+  volatile int* abort_flag = &abort_flag_s;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + STAGES * S::kStage;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
+  auto accf_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
+  auto acce_bar = [&](int b) { return bars + 8u * (2 * STAGES + NACC + b); };
+  const uint32_t done_bar = bars + 8u * (2 * STAGES + 2 * NACC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + STAGES * S::kStage + S::kBars);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const bool leader = rank == 0;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int n_units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  constexpr uint32_t kCols = (NACC * BN <= 256) ? 256u : 512u;
+  static_assert(NACC * BN <= 512, "tensor-memory columns");
+
+  if (threadIdx.x == 0) {
+    abort_flag_s = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < NACC; ++b) {
+      mbar_init(accf_bar(b), 1);
+      mbar_init(acce_bar(b), kEpiWarps * (PAIR ? 2 : 1));
+    }
+    mbar_init(done_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 0) {
+    __syncwarp();
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(tmem_slot)),
+                   "r"(kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(tmem_slot)),
+                   "r"(kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_begin();
+
+  const int n_mt = p.stats[3] / (PAIR ? 2 : 1);
+  const int total = n_mt * p.nN;
+  auto decode_at = [&](int t) {
+    return t < total ? decode8<EPI, BN, PAIR>(t, p, rank, n_mt) : Tile8{0, 0, 0, 0};
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer (both CTAs of a pair) ----------------
+      const uint64_t pol_a = policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued_parity[STAGES];
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
+      bool ok = true;
+      Tile8 nxt = decode_at(unit);
+      for (int t = unit; t < total && ok; t += n_units) {
+        const Tile8 d = nxt;
+        nxt = decode_at(t + n_units);
+        const CUtensorMap* mb = d.e >= p.E ? &mapBs : &mapB;
+        const int eb = d.e >= p.E ? 0 : d.e;
+        // pieces of A: one box of 128 rows, or up to four of 16 (single CTAs)
+        const int pieces = (PAIR || d.rows > 64) ? 0 : max(1, (d.rows + 15) / 16);
+        const uint32_t a_bytes = pieces == 0 ? S::kA : pieces * 16 * kBK;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+          const uint32_t sa = base + stage * S::kStage;
+          const uint32_t sb = sa + S::kA;
+          const uint32_t fb = full_bar(stage);
+          if (!PAIR || leader) mbar_expect_tx(fb, PAIR ? 2 * (S::kA + S::kB) : a_bytes + S::kB);
+          issued_parity[stage] = (int)phase;
+          const int k0 = kb * kBK;
+          if constexpr (PAIR) {
+            const uint32_t lfb = mapa(fb, 0);
+            tma_3d_pair_hint(sa, &mapA, lfb, k0, d.m0, 0, pol_a);
+#pragma unroll
+            for (int m = 0; m < NBM; ++m) {
+              const uint32_t sbm = sb + m * BLK * kBK;
+              // SwiGLU: this CTA holds the gate (rank 0) or the up (rank 1) rows
+              const int row = EPI == I8_SWIGLU ? (rank ? p.F : 0) + d.n0 + m * BLK
+                                               : d.n0 + m * NMM + rank * BLK;
+              tma_3d_pair(sbm, mb, lfb, k0, row, eb);
+            }
+          } else {
+            if (pieces == 0) {
+              tma_3d_hint(sa, &mapA, fb, k0, d.m0, 0, pol_a);
+            } else {
+              for (int i = 0; i < pieces; ++i)
+                tma_3d_hint(sa + i * 16 * kBK, &mapA16, fb, k0, d.m0 + 16 * i, 0, pol_a);
+            }
+            if (EPI == I8_SWIGLU) {
+              tma_3d(sb, mb, fb, k0, d.n0, eb);
+              tma_3d(sb + (BN / 2) * kBK, mb, fb, k0, p.F + d.n0, eb);
+            } else {
+              tma_3d(sb, mb, fb, k0, d.n0, eb);
+            }
+          }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // the copies this CTA's barriers track have landed before teardown
+      if (!PAIR || leader)
+        for (int s = 0; s < STAGES; ++s)
+          if (issued_parity[s] >= 0) mbar_wait(full_bar(s), (uint32_t)issued_parity[s], abort_flag);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (the pair leader only) ----------------
+    if (lane == 0 && leader) {
+      constexpr uint32_t idesc = idesc_i8(PAIR ? 2 * BM : BM, NMM);
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += n_units) {
+        if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t dt = tmem + acc * BN;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = base + stage * S::kStage;
+          const uint32_t sb = sa + S::kA;
+#pragma unroll
+          for (int ks = 0; ks < kBK / kUmmaK; ++ks) {
+            const uint64_t ad = sw128_desc(sa + ks * kUmmaK, 16, 1024);
+#pragma unroll
+            for (int m = 0; m < NBM; ++m) {
+              const uint64_t bd = sw128_desc(sb + m * BLK * kBK + ks * kUmmaK, 16, 1024);
+              if constexpr (PAIR) umma_i8_pair(dt + m * NMM, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
+              else umma_i8(dt + m * NMM, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
+            }
+          }
+          if constexpr (PAIR) umma_commit_pair_both(empty_bar(stage));
+          else umma_commit(empty_bar(stage));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if constexpr (PAIR) umma_commit_pair_both(accf_bar(acc));
+        else umma_commit(accf_bar(acc));
+        if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
+      }
+      if constexpr (PAIR) umma_commit_pair_local(done_bar);
+      else umma_commit(done_bar);
+      mbar_wait(done_bar, 0, abort_flag);
+    }
+  } else {
+    // ---------------- epilogue (warps 2..9) ----------------
+    // Two warps per TMEM lane quarter; warp half hh takes half of the columns.
+    const int q = warp & 3;
+    const int hh = (warp - 2) >> 2;
+    const uint32_t stg = base + S::kEpiOff + (warp - 2) * S::kStgW;
+    int acc = 0, box = 0;
+    uint32_t acc_phase = 0;
+    Tile8 nxt = decode_at(unit);
+    for (int t = unit; t < total; t += n_units) {
+      const Tile8 d = nxt;
+      nxt = decode_at(t + n_units);
+      const int row0 = d.m0 + q * 32;
+      const bool any = d.rows > q * 32;                 // some row of this warp holds a token
+      const bool valid = d.rows > q * 32 + lane;
+      float rs = 0.f;
+      if (valid) rs = EPI == I8_SWIGLU ? p.row_scale[row0 + lane] : scale_of(p.row_max[row0 + lane]);
+      const float* cs = d.e >= p.E ? p.col_scale_s : p.col_scale + (int64_t)d.e * p.cols;
+      bool ok = (lane == 0) ? mbar_wait(accf_bar(acc), acc_phase, abort_flag) : true;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t trow = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
+      if (any) {
+        if constexpr (EPI == I8_SWIGLU) {
+          // MMA m of the tile holds gate columns [0, NMM/2) and up columns
+          // behind them, for F columns n0 + m NMM/2 + ...
+          constexpr int HB = NMM / 2;                   // gate columns per MMA
+          constexpr int HJ = HB / 2;                    // this warp's share of them
+          unsigned big = 0;
+#pragma unroll 1
+          for (int c = 0; c < NBM * HJ; c += 32) {
+            const int m = c / HJ, j = hh * HJ + c % HJ;   // column inside the MMA's gate half
+            uint32_t ra[32], rb[32];
+            tmem_ld32(trow + m * NMM + j, ra);
+            tmem_ld32(trow + m * NMM + HB + j, rb);
+            const int f0 = d.n0 + m * HB + j;
+            const float4* ca = reinterpret_cast<const float4*>(cs + f0);
+            const float4* cb = reinterpret_cast<const float4*>(cs + p.F + f0);
+            tmem_wait();
+            float h[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 sa = __ldg(ca + i), sb = __ldg(cb + i);
+              const float wa[4] = {sa.x, sa.y, sa.z, sa.w}, wb[4] = {sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float a = __int2float_rn((int)ra[4 * i + k]) * (rs * wa[k]);
+                const float b = __int2float_rn((int)rb[4 * i + k]) * (rs * wb[k]);
+                const float v = a * fast_sigmoid(a) * b;
+                h[4 * i + k] = v;
+                big = max(big, __float_as_uint(v) & 0x7fffffffu);
+              }
+            }
+            if (lane == 0) bulk_wait_read_0();
+            __syncwarp();
+            stage_box_f32_sw128(stg, h);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&mapO, stg, f0, row0);
+              bulk_commit();
+            }
+          }
+          if (valid) atomicMax(p.row_max + row0 + lane, big);
+        } else {
+          constexpr int HC = BN / 2;
+#pragma unroll 1
+          for (int c = 0; c < HC; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(trow + hh * HC + c, r);
+            const int n = d.n0 + hh * HC + c;
+            const float4* cn = reinterpret_cast<const float4*>(cs + n);
+            tmem_wait();
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 s = __ldg(cn + i);
+              v[4 * i] = __int2float_rn((int)r[4 * i]) * (rs * s.x);
+              v[4 * i + 1] = __int2float_rn((int)r[4 * i + 1]) * (rs * s.y);
+              v[4 * i + 2] = __int2float_rn((int)r[4 * i + 2]) * (rs * s.z);
+              v[4 * i + 3] = __int2float_rn((int)r[4 * i + 3]) * (rs * s.w);
+            }
+            uint4 u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = pack8_bf16(v + 8 * j);
+            const uint32_t buf = stg + box * kTmaBox;
+            box ^= 1;
+            if (lane == 0) bulk_wait_read_1();
+            __syncwarp();
+            stage_box_sw64(buf, u);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&mapO, buf, n, row0);
+              bulk_commit();
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (!PAIR || leader) mbar_arrive(acce_bar(acc));
+        else mbar_arrive_remote(mapa(acce_bar(acc), 0));
+      }
+      if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  tc_fence_after();
+  if (warp == 0) {
+    __syncwarp();
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols)
+                   : "memory");
+  }
+}
+
+}  // namespace i8
+}  // namespace moe

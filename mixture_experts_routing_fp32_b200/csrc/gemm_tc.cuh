@@ -145,7 +145,7 @@ __device__ __forceinline__ uint64_t global_ns() {
   return t;
 }
 // Bounded wait for phase `parity` of `bar`.  False once the kernel aborted.
-__device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+static __device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                        bool cluster_acquire = false) {
   auto probe = [&] {
     return cluster_acquire ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity);

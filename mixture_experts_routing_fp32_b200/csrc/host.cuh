@@ -1,5 +1,5 @@
 // Host side shared by the library's translation units: launch counting,
-// per-launch timing and error codes.  The state behind
+// per-launch timing, error codes and tensor maps.  The state behind
 // these (thread-local) is defined in moe.cu.
 #pragma once
 #include <cuda.h>
@@ -17,6 +17,27 @@ void before_launch(cudaStream_t s);                    // timing event, if enabl
 int after_launch(cudaStream_t s, const char* name);    // counts, checks, timing event
 bool use_pdl();
 int sm_count();                                        // of the current device
+
+// cuTensorMapEncodeTiled for one- to three-dimensional tensors of 1-byte
+// elements [n3][rows][cols], 128-byte swizzle, box {128, box_rows, 1}.
+int make_map_u8(CUtensorMap* m, const void* ptr, int64_t n3, int64_t rows, int64_t cols,
+                uint32_t box_rows);
+// TMA-store targets [rows][cols]: bf16 (64-byte swizzle) or fp32 (128-byte
+// swizzle), 32 x 32 boxes.
+int make_out_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, bool fp32);
+
+// Layout facts of a layer configuration (moe_get_sizes's) for the units that
+// work on permuted rows.
+struct LayerView {
+  int64_t rows_max, tiles_max;
+  int align, local_experts;
+  bool tensor_cores;
+};
+int layer_view(const moe_config_t* c, LayerView* out);   // MOE_ERR_ARG for an invalid cfg
+
+// The error words of the other units (each has its own copy of the device
+// error word): read and cleared by moe_check_status.
+int take_i8_error(unsigned* bits);
 
 #define MOE_HCK(expr)                                          \
   do {                                                         \
@@ -58,6 +79,26 @@ int launch(const char* name, void (*kern)(KP...), dim3 grid, dim3 block, size_t 
   before_launch(s);
   MOE_HCK(cudaLaunchKernelEx(&lc, kern, std::forward<A>(args)...));
   return after_launch(s, name);
+}
+
+// Clusters of `size` CTAs of kernel k that the current device holds at once.
+template <typename K>
+int resident_clusters(K k, int size, int threads, size_t smem, int64_t* out) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.gridDim = dim3(size * (sm_count() / size));
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  int n = 0;
+  MOE_HCK(cudaOccupancyMaxActiveClusters(&n, k, &lc));
+  *out = n > 0 ? n : sm_count() / size;
+  return MOE_OK;
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

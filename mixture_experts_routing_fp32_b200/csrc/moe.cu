@@ -1,6 +1,7 @@
 // libmoe.so: the layer's extern "C" entry points declared in include/moe.h;
 // the kernels live in the .cuh files beside this one.  norm.cu holds the norms
-// around the layer, adamw.cu the optimizer step; what the units share is declared in host.cuh and defined at the end of this file.
+// around the layer, adamw.cu the optimizer step, ffn_i8.cu the experts in
+// 8-bit integers; what the units share is declared in host.cuh and defined at the end of this file.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -2069,6 +2070,9 @@ int moe_check_status(cudaStream_t s, uint32_t* bits) {
   unsigned v = 0, zero = 0;
   MOE_CK(cudaMemcpyFromSymbol(&v, moe::g_dev_error, sizeof(v)));
   MOE_CK(cudaMemcpyToSymbol(moe::g_dev_error, &zero, sizeof(zero)));
+  unsigned vi = 0;
+  MOE_TRY(moe::host::take_i8_error(&vi));
+  v |= vi;
   if (bits) *bits = v;
   return v ? MOE_ERR_DEVICE : MOE_OK;
 }
@@ -2173,6 +2177,35 @@ int after_launch(cudaStream_t s, const char* name) {
 }
 bool use_pdl() { return pdl_enabled(); }
 int sm_count() { return num_sms(); }
+
+int make_map_u8(CUtensorMap* m, const void* ptr, int64_t n3, int64_t rows, int64_t cols,
+                uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return fail(cudaErrorNotSupported);
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n3};
+  cuuint64_t strides[2] = {(cuuint64_t)cols, (cuuint64_t)(rows * cols)};
+  cuuint32_t box[3] = {128, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides,
+                        box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : fail(cudaErrorInvalidValue);
+}
+
+int make_out_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, bool fp32) {
+  return fp32 ? make_store_map_f32(m, ptr, rows, cols) : make_store_map(m, ptr, rows, cols);
+}
+
+int layer_view(const moe_config_t* c, LayerView* out) {
+  MOE_TRY(validate(c));
+  const Layout L = layout_of(c);
+  out->rows_max = L.rows_max;
+  out->tiles_max = L.tiles_max;
+  out->align = L.align;
+  out->local_experts = local_E(c);
+  out->tensor_cores = use_tc(c);
+  return MOE_OK;
+}
 
 }  // namespace host
 }  // namespace moe

@@ -21,7 +21,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC",
+    "-Xcompiler", "-fPIC", "-shared",
     "-I", os.path.join(ROOT, "include"),
     "--expt-relaxed-constexpr",
 ]
@@ -70,7 +70,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if not force and not _older(obj, _deps(u)):
             continue
         tmp = obj + ".%d.tmp.o" % os.getpid()
-        cmd = [NVCC, *FLAGS, *extra, "-c", u, "-o", tmp]
+        cmd = [NVCC, *(f for f in FLAGS if f != "-shared"), *extra, "-c", u, "-o", tmp]
         if verbose:
             print(" ".join(cmd), flush=True)
         p = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -85,7 +85,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         os.replace(tmp, obj)
     if not errors:
         tmp = OUT + ".%d.tmp" % os.getpid()
-        cmd = [NVCC, *FLAGS[:2], "-shared", "-Xcompiler", "-fPIC", *objects, "-o", tmp]
+        cmd = [NVCC, *FLAGS, *objects, "-o", tmp]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode == 0:
             os.replace(tmp, OUT)

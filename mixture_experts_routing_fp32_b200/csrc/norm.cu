@@ -18,6 +18,8 @@
 // of D/8 threads) and stream the next rows into shared memory with cp.async.
 // Each thread copies exactly the 16-byte pieces that it reads back itself,
 // so the ring needs no barrier; the only ones are those of the row sums.
+#include <type_traits>
+
 #include "host.cuh"
 
 namespace moe {
@@ -272,6 +274,13 @@ __device__ __forceinline__ int first_row(int T, int p, int P) {
 // go out as partials) and, times the gate, add to the CTA's sums for w_post,
 // which live in shared memory.  R row groups of a CTA add up through shared
 // memory at a segment's end, in group order.
+//
+// A row of 7168 columns leaves one CTA of 28 warps per SM, so what a row
+// waits for is not hidden by other rows: the vectors (w_pre, and alpha gate
+// w_post as one) sit in shared memory in the ring's layout, the row's
+// statistics are loaded a row ahead, and a tensor's values are taken from
+// the ring only where they are used (64 registers hold 16 sums and 24
+// values).
 template <typename TA, typename TR, bool BIAS>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
@@ -287,10 +296,14 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   const int o_dx = kA * pitch, o_r = 2 * kA * pitch, o_g = (2 * kA + kR) * pitch;
   uint8_t* mine = ring + tid * 16;
   const uint32_t mine_a = smem_addr(mine);
-  // after the ring: [2][D] running sums for w_post, b_post (several), and
-  // one [R][8 tpr] exchange buffer (R > 1)
-  float* w_sum = reinterpret_cast<float*>(ring + a.stages * stage_bytes);
-  float* swap = w_sum + (a.several ? 2 * a.D : 0);
+  // after the ring: this thread's 8 columns of w_pre and of alpha gate w_post,
+  // [2][D] running sums for w_post, b_post (several), and one [R][8 tpr]
+  // exchange buffer (R > 1)
+  uint8_t* v_pre = mine + a.stages * stage_bytes;
+  uint8_t* v_post = v_pre + 2 * pitch;
+  constexpr int kW = BIAS ? 2 : 1;
+  float* w_sum = reinterpret_cast<float*>(ring + a.stages * stage_bytes + 4 * pitch);
+  float* swap = w_sum + (a.several ? kW * a.D : 0);
   const TA* y = static_cast<const TA*>(a.y);
   const TA* dx = static_cast<const TA*>(a.dx);
   const TR* r = static_cast<const TR*>(a.r);
@@ -299,20 +312,32 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   const int row0 = first_row(a.T, p, P), row1 = first_row(a.T, p + 1, P);
   const int64_t arr = (int64_t)P * a.D;             // floats of one partial array
   float* part = a.part + (int64_t)p * a.D + c0;
-  const float layer = a.layer ? a.inv_d : 0.f;
 
   if (a.several && active && g == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w_sum[c0 + i] = w_sum[a.D + c0 + i] = 0.f;
+    for (int i = 0; i < 8; ++i)
+      for (int k = 0; k < kW; ++k) w_sum[k * a.D + c0 + i] = 0.f;
   }
   pdl_begin();
 
-  // rows of the current segment: [seg0, seg1), row group g takes seg0 + g, + R, ...
+  // idle threads of a row's last warp hold zeros in both vectors and in
+  // every tensor they weight, so they add nothing to the row's sums
+  auto keep = [&](uint8_t* at, const float* f) {
+    *reinterpret_cast<float4*>(at) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(at + pitch) = make_float4(f[4], f[5], f[6], f[7]);
+  };
+  {
+    float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (active && a.w_pre != nullptr) load8(a.w_pre + c0, w);
+    keep(v_pre, w);
+  }
+
+  // rows of a segment: [seg0, seg1), row group g takes seg0 + g, + R, ...
   const int L = a.several ? a.gate_len : a.T;
   auto seg_end = [&](int row) {
     return a.several ? (int)min((int64_t)row1, (int64_t)(row / L + 1) * L) : row1;
   };
-  // the row after t for this row group (row1: none)
+  // this row group's first row in the segments from s0 on (row1: none)
   auto first_in = [&](int s0) {
     while (s0 < row1) {
       const int e = seg_end(s0);
@@ -327,6 +352,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   };
   int ahead = first_in(row0), slot_in = 0;
   auto issue = [&] {
+    if (a.stages == 0) return;
     if (ahead < row1) {
       if (active) {
         const uint32_t s = mine_a + slot_in * stage_bytes;
@@ -366,90 +392,126 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
     }
   };
 
-  for (int i = 0; i < max(1, a.stages - 1); ++i) issue();
+  const float4* stats = reinterpret_cast<const float4*>(a.stats_in);
+  float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (ahead < row1) st_next = stats[ahead];
+  for (int i = 0; i < a.stages - 1; ++i) issue();
   int slot = 0;
   for (int seg0 = row0; seg0 < row1;) {
     const int seg1 = seg_end(seg0);
     const float* gate = a.gate_len > 0 ? a.gate + (int64_t)(seg0 / a.gate_len) * a.D + c0 : nullptr;
-    for (int t = seg0 + g; t < seg1; t += a.R) {
-      if (a.stages > 1) issue();
-      cp_wait(a.stages - 1);
-      const uint8_t* from = mine + slot * stage_bytes;
-      if (++slot == a.stages) slot = 0;
-      float d[8], u[8], h[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = u[i] = h[i] = 0.f;
-      float yv[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) yv[i] = 0.f;
-      const float4 st = *reinterpret_cast<const float4*>(a.stats_in + 4 * (int64_t)t);
+    if (y != nullptr) {
+      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (active) {
-        if (gin != nullptr) take<TR>(from + o_g, pitch, d);
-        if (dx != nullptr) {
-          take<TA>(from + o_dx, pitch, u);
-          take<TR>(from + o_r, pitch, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = a.alpha;
+        float o[8];
+        if (gate != nullptr) {
+          load8(gate, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] *= o[i];
         }
-        if (y != nullptr) take<TA>(from, pitch, yv);
+        if (a.w_post != nullptr) {
+          load8(a.w_post + c0, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] *= o[i];
+        }
       }
+      keep(v_post, w);
+    }
+    for (int t = seg0 + g; t < seg1; t += a.R) {
+      issue();
+      const float4 st = st_next;
+      const int tn = next_row(t);
+      if (tn < row1) st_next = stats[tn];
       const int64_t at = (int64_t)t * a.D + c0;
+      const uint8_t* from = mine + slot * stage_bytes;
+      if (a.stages > 0) {
+        cp_wait(a.stages - 1);
+        if (++slot == a.stages) slot = 0;
+      }
+      // this thread's columns of one tensor (rows that fit no ring: from
+      // global memory)
+      auto get = [&](auto* base, int off, float* f) {
+        using T = std::remove_cv_t<std::remove_pointer_t<decltype(base)>>;
+        if (a.stages > 0) take<T>(from + off, pitch, f);
+        else load8(base + at, f);
+      };
+      float d[8];
       if (dx != nullptr) {
-        float w[8];
-        load8(a.w_pre + c0, w);
+        float u[8], h[8], w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = h[i] = 0.f;
+        if (active) {
+          get(dx, o_dx, u);
+          get(r, o_r, h);
+        }
+        take<float>(v_pre, pitch, w);
         float q1 = 0.f, q2 = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          h[i] = active ? (h[i] - st.z) * st.w : 0.f;
+          h[i] = (h[i] - st.z) * st.w;
           p1[i] = fmaf(u[i], h[i], p1[i]);
           if constexpr (BIAS) p2[i] += u[i];
           u[i] *= w[i];
           q1 = fmaf(u[i], h[i], q1);
-          q2 += u[i];
         }
-        const float2 q = sum(q1, q2);
-        const float m1 = q.x * a.inv_d, m2 = q.y * layer;
+        float m2 = 0.f;
+        if (a.layer) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = fmaf(st.w, u[i] - m2 - h[i] * m1, d[i]);
-      }
-      // one stage: the slot is free once its values have been used
-      if (a.stages == 1) {
-        __syncwarp();
-        issue();
+          for (int i = 0; i < 8; ++i) q2 += u[i];
+          const float2 q = sum(q1, q2);
+          q1 = q.x;
+          m2 = q.y * a.inv_d;
+        } else {
+          q1 = sum(q1);
+        }
+        const float m1 = -q1 * a.inv_d;
+        // rstd (u - m2 - h m1) + dr_out
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = fmaf(h[i], m1, u[i] - m2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+        if (gin != nullptr && active) get(gin, o_g, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = fmaf(st.w, u[i], d[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+        if (gin != nullptr && active) get(gin, o_g, d);
       }
       if (active) store8(static_cast<TR*>(a.dr) + at, d);
       if (y != nullptr) {
-        float gw[8];
-        if (gate != nullptr) {
-          load8(gate, gw);
+        float yv[8], e[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) gw[i] *= a.alpha * d[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) gw[i] = a.alpha * d[i];
-        }
-        float q1 = 0.f, q2 = 0.f;
+        for (int i = 0; i < 8; ++i) yv[i] = 0.f;
+        if (active) get(y, 0, yv);
+        take<float>(v_post, pitch, e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          yv[i] = active ? (yv[i] - st.x) * st.y : 0.f;
-          if (active) {
-            s1[i] = fmaf(d[i], yv[i], s1[i]);
-            if constexpr (BIAS) s2[i] += d[i];
-          }
+          yv[i] = (yv[i] - st.x) * st.y;
+          s1[i] = fmaf(d[i], yv[i], s1[i]);
+          if constexpr (BIAS) s2[i] += d[i];
+          e[i] *= d[i];
         }
         if (a.w_post != nullptr) {
-          float w[8];
-          load8(a.w_post + c0, w);
+          float q1 = 0.f, q2 = 0.f, m2 = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            gw[i] = active ? gw[i] * w[i] : 0.f;
-            q1 = fmaf(gw[i], yv[i], q1);
-            q2 += gw[i];
+          for (int i = 0; i < 8; ++i) q1 = fmaf(e[i], yv[i], q1);
+          if (a.layer) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q2 += e[i];
+            const float2 q = sum(q1, q2);
+            q1 = q.x;
+            m2 = q.y * a.inv_d;
+          } else {
+            q1 = sum(q1);
           }
-          const float2 q = sum(q1, q2);
-          const float m1 = q.x * a.inv_d, m2 = q.y * layer;
+          const float m1 = -q1 * a.inv_d;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) gw[i] = st.y * (gw[i] - m2 - yv[i] * m1);
+          for (int i = 0; i < 8; ++i) e[i] = st.y * fmaf(yv[i], m1, e[i] - m2);
         }
-        if (active) store8(static_cast<TA*>(a.dy) + at, gw);
+        if (active) store8(static_cast<TA*>(a.dy) + at, e);
       }
     }
     if (a.several) {
@@ -530,13 +592,14 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   }
 }
 
-// Adds the partials up in CTA order: 32 columns a block, 32 strands of
-// partials joined in strand order.  blockIdx.y = 0: the weights' and biases'
-// gradients (and the gate's, when it has one row); blockIdx.y = q > 0: the
-// gate row cut at the start of CTA q, if q is the first cut in it.
+// Adds the partials up: 32 columns a block, 32 strands of partials joined by
+// a warp.  blockIdx.y = 0: the weights' and biases' gradients (and the
+// gate's, when it has one row); blockIdx.y > 0: a gate row that CTAs cut.
+// With fewer gate rows than CTAs, y - 1 is the gate row; else y is a CTA, and
+// the gate row is the one cut at its start.
 struct SumArgs {
   NormArgs n;
-  int P;
+  int P, by_row;
   float *dw_post, *db_post, *dw_pre, *db_pre;
 };
 
@@ -548,66 +611,74 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const SumArgs s) {
   const bool in = col < a.D;
   const int64_t arr = (int64_t)s.P * a.D;
   pdl_begin();
-  auto add = [&](int which) {
+  // over CTAs [p0, p1) of array `which` (the same in every thread of a column)
+  auto add = [&](int which, int p0, int p1) {
+    const float* at = a.part + which * arr + col;
     float v = 0.f;
-    if (in)
-      for (int p = strand; p < s.P; p += 32) v += a.part[which * arr + (int64_t)p * a.D + col];
+    if (in) {
+#pragma unroll 4
+      for (int p = p0 + strand; p < p1; p += 32) v += at[(int64_t)p * a.D];
+    }
     __syncthreads();
     tile[strand][cx] = v;
     __syncthreads();
-    float t = tile[cx][strand];     // transposed: the warp's 32 strands of column `strand`
+    float t = tile[cx][strand];     // the warp's 32 strands of column `strand`
     t = warp_sum(t);
     __syncthreads();
     if (cx == 0) tile[0][strand] = t;
     __syncthreads();
     return tile[0][cx];
   };
+  auto gate_grad = [&](float s1, float s2) {
+    float o = a.w_post != nullptr ? a.w_post[col] * s1 : s1;
+    if (a.b_post != nullptr) o = fmaf(a.b_post[col], s2, o);
+    return a.alpha * o;
+  };
   if (blockIdx.y == 0) {
     const bool bias_y = s.db_post != nullptr || (a.dgate != nullptr && a.b_post != nullptr);
-    if (a.y != nullptr) {
-      const float s1 = add(a.several ? W1 : S1H);
-      const float s2 = bias_y ? add(a.several ? W2 : S2H) : 0.f;
+    if (a.y != nullptr && (s.dw_post != nullptr || s.db_post != nullptr || !a.several)) {
+      const float s1 = add(a.several ? W1 : S1H, 0, s.P);
+      const float s2 = bias_y ? add(a.several ? W2 : S2H, 0, s.P) : 0.f;
       if (in && strand == 0) {
         // several gate rows: the sums already hold the gate
         const float gate = (a.gate_len > 0 && !a.several) ? a.gate[col] : 1.f;
         if (s.dw_post != nullptr) s.dw_post[col] = a.alpha * gate * s1;
         if (s.db_post != nullptr) s.db_post[col] = a.alpha * gate * s2;
-        if (a.dgate != nullptr && !a.several) {
-          float o = a.w_post != nullptr ? a.w_post[col] * s1 : s1;
-          if (a.b_post != nullptr) o = fmaf(a.b_post[col], s2, o);
-          a.dgate[col] = a.alpha * o;
-        }
+        if (a.dgate != nullptr && !a.several) a.dgate[col] = gate_grad(s1, s2);
       }
     }
-    if (a.dx != nullptr) {
-      const float v = add(P1);
-      if (in && strand == 0 && s.dw_pre != nullptr) s.dw_pre[col] = v;
-      if (s.db_pre != nullptr) {
-        const float b = add(P2);
-        if (in && strand == 0) s.db_pre[col] = b;
-      }
+    if (s.dw_pre != nullptr) {
+      const float v = add(P1, 0, s.P);
+      if (in && strand == 0) s.dw_pre[col] = v;
+    }
+    if (s.db_pre != nullptr) {
+      const float b = add(P2, 0, s.P);
+      if (in && strand == 0) s.db_pre[col] = b;
     }
     return;
   }
-  // a gate row cut by CTA boundaries: tail of the CTA that starts it, then
-  // the heads of the CTAs that go on with it
-  if (a.dgate == nullptr) return;
-  const int q = blockIdx.y;
-  const int cut = first_row(a.T, q, s.P);
-  const int gr = cut / a.gate_len;
-  const int64_t gs = (int64_t)gr * a.gate_len, ge = min((int64_t)a.T, gs + a.gate_len);
-  if (gs == cut || first_row(a.T, q - 1, s.P) > gs) return;   // not cut, or not its first cut
-  if (!in || strand != 0) return;
-  const float* at = a.part + col;
-  float s1 = at[S1T * arr + (int64_t)(q - 1) * a.D];
-  float s2 = a.b_post != nullptr ? at[S2T * arr + (int64_t)(q - 1) * a.D] : 0.f;
-  for (int k = q; k < s.P && first_row(a.T, k, s.P) < ge; ++k) {
-    s1 += at[S1H * arr + (int64_t)k * a.D];
-    if (a.b_post != nullptr) s2 += at[S2H * arr + (int64_t)k * a.D];
+  // The CTA that starts the gate row left its share as its tail, those that
+  // go on with it as their heads.
+  int64_t gs;
+  if (s.by_row) {
+    gs = (int64_t)(blockIdx.y - 1) * a.gate_len;
+  } else {
+    const int cut = first_row(a.T, blockIdx.y, s.P);
+    gs = (int64_t)(cut / a.gate_len) * a.gate_len;
+    if (gs == cut || first_row(a.T, blockIdx.y - 1, s.P) > gs) return;   // not its first cut
   }
-  float o = a.w_post != nullptr ? a.w_post[col] * s1 : s1;
-  if (a.b_post != nullptr) o = fmaf(a.b_post[col], s2, o);
-  a.dgate[(int64_t)gr * a.D + col] = a.alpha * o;
+  const int64_t ge = min((int64_t)a.T, gs + a.gate_len);
+  auto holder = [&](int64_t row) { return (int)(((row + 1) * s.P - 1) / a.T); };
+  const int pa = holder(gs), pb = holder(ge - 1);
+  if (pa == pb) return;                        // whole in one CTA: written there
+  // (a row that ends where its last CTA does is cut all the same)
+  float s1 = add(S1H, pa + 1, pb + 1);
+  float s2 = a.b_post != nullptr ? add(S2H, pa + 1, pb + 1) : 0.f;
+  if (!in || strand != 0) return;
+  const float* at = a.part + (int64_t)pa * a.D + col;
+  s1 += at[S1T * arr];
+  if (a.b_post != nullptr) s2 += at[S2T * arr];
+  a.dgate[gs / a.gate_len * a.D + col] = gate_grad(s1, s2);
 }
 
 // ---------------------------------------------------------------------------
@@ -626,11 +697,23 @@ int check(const moe_norm_config_t* c) {
 
 bool several_rows(const moe_norm_config_t* c) { return c->gate_len > 0 && c->gate_len < c->T; }
 int threads_per_row(int D) { return (int)(host::ceil_div(D / 8, 32) * 32); }
-// CTAs an SM holds in the backward: one when a row takes more than half of
-// its threads (the column sums fill the register file), else two.
-int bwd_ctas(const moe_norm_config_t* c) {
-  const int per_sm = threads_per_row(c->D) > 512 ? 1 : 2;
-  return (int)std::min<int64_t>(c->T, (int64_t)kSms * per_sm);
+// Row groups of a CTA of about `threads` threads (at most 15: a named
+// barrier each; single-warp groups need none, up to 16).
+int row_groups(int tpr, int threads) {
+  return std::max(1, std::min(threads / tpr, tpr == 32 ? 16 : 15));
+}
+// The backward's CTAs and their row groups.  An SM holds one CTA when a row
+// takes more than half of its threads (the column sums fill the register
+// file), else two of up to 512 threads.  Row groups share a CTA's partial
+// sums, so short batches run fewer CTAs rather than CTAs of one group; with
+// short gate segments, which a CTA's groups share, each needs four rows.
+void bwd_shape(const moe_norm_config_t* c, int* ctas, int* groups) {
+  const int tpr = threads_per_row(c->D);
+  const int64_t most = (int64_t)kSms * (tpr > 512 ? 1 : 2);
+  int64_t R = row_groups(tpr, 512);
+  if (several_rows(c)) R = std::max<int64_t>(1, std::min<int64_t>(R, c->gate_len / 4));
+  *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most, host::ceil_div(c->T, R)));
+  *groups = (int)std::min<int64_t>(R, host::ceil_div(c->T, *ctas));
 }
 
 NormArgs args_of(const moe_norm_config_t* c) {
@@ -640,11 +723,6 @@ NormArgs args_of(const moe_norm_config_t* c) {
   a.gate_len = c->gate_len; a.eps = c->eps; a.alpha = c->alpha;
   a.inv_d = 1.0f / (float)c->D;
   return a;
-}
-// Row groups of a CTA of about `threads` threads (at most 15: a named
-// barrier each; single-warp groups need none, up to 16).
-int row_groups(int tpr, int threads) {
-  return std::max(1, std::min(threads / tpr, tpr == 32 ? 16 : 15));
 }
 template <typename... P>
 bool any_misaligned(P... p) {
@@ -672,21 +750,31 @@ int forward(NormArgs a, cudaStream_t s) {
 template <typename TA, typename TR, bool BIAS>
 int backward(NormArgs a, int P, SumArgs& sum, cudaStream_t s) {
   auto k = block_norm_bwd_kernel<TA, TR, BIAS>;
-  // row groups only where a segment gives each of them several rows
-  a.R = row_groups(a.tpr, 512);
-  const int64_t rows = a.several ? std::min<int64_t>(a.gate_len, a.T / P) : a.T / P;
-  a.R = (int)std::max<int64_t>(1, std::min<int64_t>(a.R, rows / (a.several ? 4 : 1)));
   const int threads = a.R * a.tpr;
   const size_t stage = 2 * (size_t)(kPiece<TA> + kPiece<TR>) * threads;
-  const size_t fixed = (a.several ? 2 * (size_t)a.D * 4 : 0) + (a.R > 1 ? (size_t)threads * 32 : 0);
-  const size_t room = (kSmemLimit - 9 * 1024 * 2) / (threads > 512 ? 1 : 2) - fixed;
-  a.stages = (int)std::max<size_t>(1, std::min<size_t>(3, room / stage));
+  const size_t fixed = (size_t)threads * 64 + (a.several ? (BIAS ? 2 : 1) * (size_t)a.D * 4 : 0) +
+                       (a.R > 1 ? (size_t)threads * 32 : 0);
+  // two CTAs an SM share its shared memory (8 KB static and 1 KB of the
+  // system's each)
+  const size_t room = (threads > 512 ? kSmemLimit : kSmemLimit / 2) - 9 * 1024 - fixed;
+  // a ring of one stage would overlap nothing: rows too long for two (wide
+  // fp32 rows) are read where they are used
+  a.stages = (int)std::min<size_t>(3, room / stage);
+  if (a.stages < 2) a.stages = 0;
   const size_t smem = a.stages * stage + fixed;
   MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit - 9 * 1024));
   MOE_HTRY(host::launch("block_norm_bwd", k, P, threads, smem, s, 1, a));
   sum.n = a;
   sum.P = P;
-  const dim3 grid((unsigned)host::ceil_div(a.D, 32), a.several && a.dgate != nullptr ? P : 1);
+  // dgate of the gate rows that CTAs cut: by gate row where there are fewer
+  // of those than CTAs, else by CTA
+  int cuts = 0;
+  if (a.several && a.dgate != nullptr) {
+    const int64_t rows = host::ceil_div(a.T, a.gate_len);
+    sum.by_row = rows < P;
+    cuts = (int)std::min<int64_t>(rows, P - 1);
+  }
+  const dim3 grid((unsigned)host::ceil_div(a.D, 32), 1 + cuts);
   return host::launch("block_norm_sum", block_norm_sum_kernel, grid, 1024, 0, s, 1, sum);
 }
 
@@ -720,7 +808,9 @@ int moe_block_norm(const moe_norm_config_t* c, const void* r, const void* y,
 
 int64_t moe_block_norm_ws_bytes(const moe_norm_config_t* c) {
   if (check(c) != MOE_OK) return 0;
-  return (int64_t)bwd_ctas(c) * c->D * 4 * (several_rows(c) ? 8 : 4);
+  int ctas = 0, groups = 0;
+  bwd_shape(c, &ctas, &groups);
+  return (int64_t)ctas * c->D * 4 * (several_rows(c) ? 8 : 4);
 }
 
 int moe_block_norm_backward(const moe_norm_config_t* c, const void* r_out, const void* y,
@@ -748,7 +838,8 @@ int moe_block_norm_backward(const moe_norm_config_t* c, const void* r_out, const
   a.several = y != nullptr && several_rows(c);
   SumArgs sum{};
   sum.dw_post = dw_post; sum.db_post = db_post; sum.dw_pre = dw_pre; sum.db_pre = db_pre;
-  const int P = bwd_ctas(c);
+  int P = 0;
+  bwd_shape(c, &P, &a.R);
   const bool bias = db_post != nullptr || db_pre != nullptr || (dgate != nullptr && b_post != nullptr);
   auto go = [&](auto ta, auto tr) {
     using TA = decltype(ta);

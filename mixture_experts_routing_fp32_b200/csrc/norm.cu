@@ -29,6 +29,7 @@ constexpr int kMaxD = 8192;          // 1024 threads of 8 columns
 constexpr int kMaxThreads = 1024;
 constexpr int kSms = 148;            // the backward's partial sums are sized for this grid
 constexpr size_t kSmemLimit = 227 * 1024;
+constexpr int kDynSmem = (int)kSmemLimit - 8 * 1024;   // beside the row sums' static 8 KB
 
 struct NormArgs {
   int T, D, nv, tpr, R, stages;      // nv = D / 8; tpr threads a row, R rows at once in a CTA
@@ -78,26 +79,121 @@ __device__ __forceinline__ void fetch(uint32_t slot, int pitch, const T* p) {
   cp16(slot, p);
   if constexpr (sizeof(T) == 4) cp16(slot + pitch, p + 4);
 }
-template <typename T>
-__device__ __forceinline__ void take(const uint8_t* slot, int pitch, float* f);
-template <>
-__device__ __forceinline__ void take<__nv_bfloat16>(const uint8_t* slot, int, float* f) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(slot), f);
+// 8 fp32 values as four register pairs: fma.rn.f32x2 and its like work on a
+// pair in one instruction, each half rounded as the scalar form (these
+// kernels issue close to an instruction per cycle, so this is what lets them
+// reach DRAM's rate).
+struct F8 {
+  uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-template <>
-__device__ __forceinline__ void take<float>(const uint8_t* slot, int pitch, float* f) {
-  const float4 a = *reinterpret_cast<const float4*>(slot);
-  const float4 b = *reinterpret_cast<const float4*>(slot + pitch);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F8 zero8f() { return F8{{0ull, 0ull, 0ull, 0ull}}; }
+// a * b + c, with b and c one value for all (or a pair of them)
+__device__ __forceinline__ F8 fma8(const F8& a, uint64_t b, uint64_t c) {
+  return F8{{fma2(a.p[0], b, c), fma2(a.p[1], b, c), fma2(a.p[2], b, c), fma2(a.p[3], b, c)}};
+}
+__device__ __forceinline__ F8 fma8(const F8& a, uint64_t b, const F8& c) {
+  return F8{{fma2(a.p[0], b, c.p[0]), fma2(a.p[1], b, c.p[1]), fma2(a.p[2], b, c.p[2]),
+             fma2(a.p[3], b, c.p[3])}};
+}
+__device__ __forceinline__ F8 fma8(const F8& a, const F8& b, const F8& c) {
+  return F8{{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1]),
+             fma2(a.p[2], b.p[2], c.p[2]), fma2(a.p[3], b.p[3], c.p[3])}};
+}
+__device__ __forceinline__ F8 mul8(const F8& a, const F8& b) {
+  return F8{{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1]), mul2(a.p[2], b.p[2]),
+             mul2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ F8 mul8(const F8& a, uint64_t b) {
+  return F8{{mul2(a.p[0], b), mul2(a.p[1], b), mul2(a.p[2], b), mul2(a.p[3], b)}};
+}
+__device__ __forceinline__ F8 add8(const F8& a, const F8& b) {
+  return F8{{add2(a.p[0], b.p[0]), add2(a.p[1], b.p[1]), add2(a.p[2], b.p[2]),
+             add2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ F8 add8(const F8& a, uint64_t b) {
+  return F8{{add2(a.p[0], b), add2(a.p[1], b), add2(a.p[2], b), add2(a.p[3], b)}};
+}
+__device__ __forceinline__ float dot8(const F8& a, const F8& b) {
+  const float2 f = unpack2(fma2(a.p[3], b.p[3], fma2(a.p[2], b.p[2],
+                                fma2(a.p[1], b.p[1], mul2(a.p[0], b.p[0])))));
+  return f.x + f.y;
+}
+__device__ __forceinline__ float sum8(const F8& a) {
+  const float2 f = unpack2(add2(add2(a.p[0], a.p[1]), add2(a.p[2], a.p[3])));
+  return f.x + f.y;
+}
+__device__ __forceinline__ F8 widen8(const uint4& u) {
+  auto two = [](uint32_t w) {
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  };
+  return F8{{two(u.x), two(u.y), two(u.z), two(u.w)}};
+}
+__device__ __forceinline__ F8 f8_of(const float4& a, const float4& b) {
+  return F8{{pack2(a.x, a.y), pack2(a.z, a.w), pack2(b.x, b.y), pack2(b.z, b.w)}};
+}
+__device__ __forceinline__ F8 load_f8(const __nv_bfloat16* p) {
+  return widen8(*reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ F8 load_f8(const float* p) {
+  return f8_of(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4));
+}
+__device__ __forceinline__ void store_f8(float* p, const F8& a) {
+  const float2 q0 = unpack2(a.p[0]), q1 = unpack2(a.p[1]), q2 = unpack2(a.p[2]), q3 = unpack2(a.p[3]);
+  *reinterpret_cast<float4*>(p) = make_float4(q0.x, q0.y, q1.x, q1.y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(q2.x, q2.y, q3.x, q3.y);
+}
+__device__ __forceinline__ uint4 narrow8(const F8& a) {
+  uint4 u;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2(a.p[i]);
+    h[i] = __floats2bfloat162_rn(f.x, f.y);
+  }
+  return u;
+}
+__device__ __forceinline__ void store_f8(__nv_bfloat16* p, const F8& a) {
+  *reinterpret_cast<uint4*>(p) = narrow8(a);
 }
 
-// The rounded values of 8 columns (what a reader of the stored row sees).
-__device__ __forceinline__ void round8(const __nv_bfloat16*, float* f) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __bfloat162float(__float2bfloat16_rn(f[i]));
+// This thread's piece back from its slot (bf16 rows use one 16-byte chunk,
+// fp32 rows two).
+template <typename T>
+__device__ __forceinline__ F8 take(const uint8_t* slot, int pitch) {
+  if constexpr (sizeof(T) == 2) return widen8(*reinterpret_cast<const uint4*>(slot));
+  else return f8_of(*reinterpret_cast<const float4*>(slot),
+                    *reinterpret_cast<const float4*>(slot + pitch));
 }
-__device__ __forceinline__ void round8(const float*, float*) {}
+__device__ __forceinline__ void keep(uint8_t* slot, int pitch, const F8& a) {
+  const float2 q0 = unpack2(a.p[0]), q1 = unpack2(a.p[1]), q2 = unpack2(a.p[2]), q3 = unpack2(a.p[3]);
+  *reinterpret_cast<float4*>(slot) = make_float4(q0.x, q0.y, q1.x, q1.y);
+  *reinterpret_cast<float4*>(slot + pitch) = make_float4(q2.x, q2.y, q3.x, q3.y);
+}
 
 // Sums of a and b over the tpr threads of a row group (all get them, in the
 // same order).  `buf` alternates, so one barrier per sum is enough: a warp
@@ -127,39 +223,37 @@ struct RowSum {
   }
 };
 
+// First row of CTA p of P (even split).
+__device__ __forceinline__ int first_row(int T, int p, int P) {
+  return (int)((int64_t)T * p / P);
+}
+
 // mean and rstd of a row held 8 values a thread (zeros in idle threads).
 // The variance is that of the centred values (a second sum), so a mean that
 // is large against the spread costs no digits.
-__device__ __forceinline__ float2 moments(const float* v, bool active, const NormArgs& a,
+__device__ __forceinline__ float2 moments(const F8& v, bool active, const NormArgs& a,
                                           RowSum& sum) {
-  float mean = 0.f;
-  if (a.layer) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += v[i];
-    mean = sum(s) * a.inv_d;
-  }
-  float q = 0.f;
-  if (active) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = v[i] - mean;
-      q = fmaf(d, d, q);
-    }
-  }
-  return make_float2(mean, rsqrtf(sum(q) * a.inv_d + a.eps));
+  if (!a.layer) return make_float2(0.f, rsqrtf(fmaf(sum(dot8(v, v)), a.inv_d, a.eps)));
+  const float mean = sum(sum8(v)) * a.inv_d;
+  const F8 d = add8(v, pack2(-mean, -mean));
+  return make_float2(mean, rsqrtf(fmaf(sum(active ? dot8(d, d) : 0.f), a.inv_d, a.eps)));
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename TA, typename TR>
+// A CTA walks a run of consecutive rows, R at a time.  The vectors stay in
+// shared memory, each thread's own 8 columns: w_pre, alpha gate w_post and,
+// with BIAS, b_pre and alpha gate b_post; those with the gate are formed
+// again when the gate row changes.  FULL: D is a multiple of 256, every
+// thread of a row holds columns.
+template <typename TA, typename TR, bool BIAS, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red_s[16 * 64];
   const int tid = threadIdx.x;
-  const int g = tid / a.tpr, vec = tid - g * a.tpr;
-  const bool active = vec < a.nv;
+  const int g = a.R == 1 ? 0 : tid / a.tpr, vec = tid - g * a.tpr;
+  const bool active = FULL || vec < a.nv;
   const int c0 = active ? vec * 8 : 0;
   RowSum sum{red_s + g * 64, a.tpr >> 5, vec >> 5, tid & 31, 1 + g, a.tpr, 0};
   const int pitch = blockDim.x * 16;
@@ -168,91 +262,90 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
   const int r_off = (kPiece<TA> / 16) * pitch;
   uint8_t* mine = ring + tid * 16;
   const uint32_t mine_a = smem_addr(mine);
+  uint8_t* v_pre = mine + a.stages * stage_bytes;
+  uint8_t *v_post = v_pre + 2 * pitch, *v_bpre = v_pre + 4 * pitch, *v_bpost = v_pre + 6 * pitch;
   const TA* y = static_cast<const TA*>(a.y);
   const TR* r = static_cast<const TR*>(a.r);
-  const int step = gridDim.x * a.R;
+  const int row0 = first_row(a.T, blockIdx.x, gridDim.x) + g;
+  const int row1 = first_row(a.T, blockIdx.x + 1, gridDim.x);
   pdl_begin();
 
-  int ahead = blockIdx.x * a.R + g, slot_in = 0;
+  int ahead = row0;
+  uint32_t slot_in = mine_a;
+  const uint32_t ring_end = mine_a + a.stages * stage_bytes;
   auto issue = [&] {
-    if (ahead < a.T && active) {
-      const uint32_t s = mine_a + slot_in * stage_bytes;
+    if (ahead < row1 && active) {
       const int64_t at = (int64_t)ahead * a.D + c0;
-      if (y != nullptr) fetch<TA>(s, pitch, y + at);
-      fetch<TR>(s + r_off, pitch, r + at);
+      if (y != nullptr) fetch<TA>(slot_in, pitch, y + at);
+      fetch<TR>(slot_in + r_off, pitch, r + at);
     }
     cp_commit();
-    ahead += step;
-    if (++slot_in == a.stages) slot_in = 0;
+    ahead += a.R;
+    slot_in += stage_bytes;
+    if (slot_in == ring_end) slot_in = mine_a;
   };
   for (int i = 0; i < a.stages - 1; ++i) issue();
-  int slot = 0;
-  for (int t = blockIdx.x * a.R + g; t < a.T; t += step) {
-    issue();
-    cp_wait(a.stages - 1);
-    float v[8], z[8];
-    const uint8_t* from = mine + slot * stage_bytes;
-    if (++slot == a.stages) slot = 0;
+  if (a.w_pre != nullptr) keep(v_pre, pitch, active ? load_f8(a.w_pre + c0) : zero8f());
+  if (BIAS && a.w_pre != nullptr)
+    keep(v_bpre, pitch, active && a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
+  // alpha gate w_post and alpha gate b_post of gate row gr
+  auto post_vectors = [&](int gr) {
+    F8 e = fma8(zero8f(), 0ull, pack2(a.alpha, a.alpha)), eb = zero8f();
     if (active) {
-      take<TR>(from + r_off, pitch, v);
-      if (y != nullptr) take<TA>(from, pitch, z);
+      if (a.gate_len > 0) e = mul8(e, load_f8(a.gate + (int64_t)gr * a.D + c0));
+      if (BIAS && a.b_post != nullptr) eb = mul8(e, load_f8(a.b_post + c0));
+      if (a.w_post != nullptr) e = mul8(e, load_f8(a.w_post + c0));
     }
-    if (!active || y == nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = 0.f;
+    keep(v_post, pitch, e);
+    if (BIAS) keep(v_bpost, pitch, eb);
+  };
+  int gate_row = -1;
+  const uint8_t* slot = mine;
+  for (int t = row0; t < row1; t += a.R) {
+    issue();
+    if (y != nullptr) {
+      const int gr = a.gate_len > 0 ? t / a.gate_len : 0;
+      if (gr != gate_row) post_vectors(gate_row = gr);
     }
-    if (!active) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
+    cp_wait(a.stages - 1);
+    F8 v = zero8f();
     const int64_t at = (int64_t)t * a.D + c0;
     float2 my = make_float2(0.f, 1.f), mr = make_float2(0.f, 1.f);
+    if (active) v = take<TR>(slot + r_off, pitch);
     if (y != nullptr) {
+      F8 z = zero8f();
+      if (active) z = take<TA>(slot, pitch);
       if (a.w_post != nullptr) {
         my = moments(z, active, a, sum);
-        float w[8];
-        load8(a.w_post + c0, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = (z[i] - my.x) * my.y * w[i];
-        if (a.b_post != nullptr) {
-          load8(a.b_post + c0, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] += w[i];
-        }
+        const float c = -my.x * my.y;
+        z = fma8(z, pack2(my.y, my.y), pack2(c, c));
       }
-      if (a.gate_len > 0) {
-        float w[8];
-        load8(a.gate + (int64_t)(t / a.gate_len) * a.D + c0, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] *= w[i];
+      if (BIAS) v = add8(v, take<float>(v_bpost, pitch));
+      v = fma8(z, take<float>(v_post, pitch), v);
+      TR* out = static_cast<TR*>(a.r_out) + at;
+      // the second norm reads the stream as it is stored: the backward then
+      // sees the same values
+      if constexpr (sizeof(TR) == 2) {
+        const uint4 u = narrow8(v);
+        if (active) *reinterpret_cast<uint4*>(out) = u;
+        v = widen8(u);
+      } else {
+        if (active) store_f8(out, v);
       }
-      if (active) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(a.alpha, z[i], v[i]);
-        TR* out = static_cast<TR*>(a.r_out) + at;
-        store8(out, v);
-        // the second norm reads the stream as it is stored: the backward
-        // then sees the same values
-        round8(out, v);
-      }
+      if (!FULL && !active) v = zero8f();
     }
     if (a.w_pre != nullptr) {
       mr = moments(v, active, a, sum);
-      if (active) {
-        float w[8];
-        load8(a.w_pre + c0, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (v[i] - mr.x) * mr.y * w[i];
-        if (a.b_pre != nullptr) {
-          load8(a.b_pre + c0, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += w[i];
-        }
-        store8(static_cast<TA*>(a.x) + at, v);
-      }
+      const float c = -mr.x * mr.y;
+      v = fma8(v, pack2(mr.y, mr.y), pack2(c, c));
+      if (BIAS) v = fma8(v, take<float>(v_pre, pitch), take<float>(v_bpre, pitch));
+      else v = mul8(v, take<float>(v_pre, pitch));
+      if (active) store_f8(static_cast<TA*>(a.x) + at, v);
     }
     if (a.stats != nullptr && vec == 0)
       *reinterpret_cast<float4*>(a.stats + 4 * (int64_t)t) = make_float4(my.x, my.y, mr.x, mr.y);
+    slot += stage_bytes;
+    if (smem_addr(slot) == ring_end) slot = mine;
   }
   cp_wait(0);
 }
@@ -260,15 +353,11 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// First row of CTA p of P (even split).
-__device__ __forceinline__ int first_row(int T, int p, int P) {
-  return (int)((int64_t)T * p / P);
-}
-
 // The column sums over tokens stay in registers while a CTA walks its rows
-// (8 columns a thread: sums of d yh and dx rh, with BIAS also of d and dx)
+// (8 columns a thread: sums of d yh and dx rh, in the general form also of
+// d and dx)
 // and leave as one partial per CTA, which block_norm_sum_kernel adds up in
-// CTA order.  When gate rows change inside the batch (`several`), the rows
+// CTA order.  When gate rows change inside the batch (SEVERAL), the rows
 // run in segments of one gate row: at a segment's end its sums of d yh and d
 // give dgate (complete segments are written here, those cut by a CTA's ends
 // go out as partials) and, times the gate, add to the CTA's sums for w_post,
@@ -281,29 +370,29 @@ __device__ __forceinline__ int first_row(int T, int p, int P) {
 // statistics are loaded a row ahead, and a tensor's values are taken from
 // the ring only where they are used (64 registers hold 16 sums and 24
 // values).
-template <typename TA, typename TR, bool BIAS>
+// GENERAL: LayerNorm, or sums for biases; else RMSNorm without them.
+template <typename TA, typename TR, bool GENERAL, bool SEVERAL, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red_s[16 * 64];
   const int tid = threadIdx.x;
-  const int g = tid / a.tpr, vec = tid - g * a.tpr;
-  const bool active = vec < a.nv;
+  const int g = a.R == 1 ? 0 : tid / a.tpr, vec = tid - g * a.tpr;
+  const bool active = FULL || vec < a.nv;
   const int c0 = active ? vec * 8 : 0;
   RowSum sum{red_s + g * 64, a.tpr >> 5, vec >> 5, tid & 31, 1 + g, a.tpr, 0};
   const int pitch = blockDim.x * 16;
-  constexpr int kA = kPiece<TA> / 16, kR = kPiece<TR> / 16;
+  constexpr int kA = kPiece<TA> / 16, kR = kPiece<TR> / 16, kW = GENERAL ? 2 : 1;
   const int stage_bytes = 2 * (kA + kR) * pitch;
   const int o_dx = kA * pitch, o_r = 2 * kA * pitch, o_g = (2 * kA + kR) * pitch;
   uint8_t* mine = ring + tid * 16;
   const uint32_t mine_a = smem_addr(mine);
   // after the ring: this thread's 8 columns of w_pre and of alpha gate w_post,
-  // [2][D] running sums for w_post, b_post (several), and one [R][8 tpr]
+  // [kW][D] running sums for w_post, b_post (SEVERAL), and one [R][8 tpr]
   // exchange buffer (R > 1)
   uint8_t* v_pre = mine + a.stages * stage_bytes;
   uint8_t* v_post = v_pre + 2 * pitch;
-  constexpr int kW = BIAS ? 2 : 1;
   float* w_sum = reinterpret_cast<float*>(ring + a.stages * stage_bytes + 4 * pitch);
-  float* swap = w_sum + (a.several ? kW * a.D : 0);
+  float* swap = w_sum + (SEVERAL ? kW * a.D : 0);
   const TA* y = static_cast<const TA*>(a.y);
   const TA* dx = static_cast<const TA*>(a.dx);
   const TR* r = static_cast<const TR*>(a.r);
@@ -313,29 +402,15 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   const int64_t arr = (int64_t)P * a.D;             // floats of one partial array
   float* part = a.part + (int64_t)p * a.D + c0;
 
-  if (a.several && active && g == 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      for (int k = 0; k < kW; ++k) w_sum[k * a.D + c0 + i] = 0.f;
+  if (SEVERAL && active && g == 0) {
+    for (int k = 0; k < kW; ++k) store_f8(w_sum + k * a.D + c0, zero8f());
   }
   pdl_begin();
 
-  // idle threads of a row's last warp hold zeros in both vectors and in
-  // every tensor they weight, so they add nothing to the row's sums
-  auto keep = [&](uint8_t* at, const float* f) {
-    *reinterpret_cast<float4*>(at) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(at + pitch) = make_float4(f[4], f[5], f[6], f[7]);
-  };
-  {
-    float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (active && a.w_pre != nullptr) load8(a.w_pre + c0, w);
-    keep(v_pre, w);
-  }
-
   // rows of a segment: [seg0, seg1), row group g takes seg0 + g, + R, ...
-  const int L = a.several ? a.gate_len : a.T;
+  const int L = SEVERAL ? a.gate_len : a.T;
   auto seg_end = [&](int row) {
-    return a.several ? (int)min((int64_t)row1, (int64_t)(row / L + 1) * L) : row1;
+    return SEVERAL ? (int)min((int64_t)row1, (int64_t)(row / L + 1) * L) : row1;
   };
   // this row group's first row in the segments from s0 on (row1: none)
   auto first_in = [&](int s0) {
@@ -347,77 +422,61 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
     return row1;
   };
   auto next_row = [&](int t) {
+    if constexpr (!SEVERAL) return min(t + a.R, row1);
     const int e = seg_end(t);
     return t + a.R < e ? t + a.R : first_in(e);
   };
-  int ahead = first_in(row0), slot_in = 0;
+  int ahead = first_in(row0);
+  uint32_t slot_in = mine_a;
+  const uint32_t ring_end = mine_a + a.stages * stage_bytes;
   auto issue = [&] {
     if (a.stages == 0) return;
     if (ahead < row1) {
       if (active) {
-        const uint32_t s = mine_a + slot_in * stage_bytes;
         const int64_t at = (int64_t)ahead * a.D + c0;
-        if (y != nullptr) fetch<TA>(s, pitch, y + at);
+        if (y != nullptr) fetch<TA>(slot_in, pitch, y + at);
         if (dx != nullptr) {
-          fetch<TA>(s + o_dx, pitch, dx + at);
-          fetch<TR>(s + o_r, pitch, r + at);
+          fetch<TA>(slot_in + o_dx, pitch, dx + at);
+          fetch<TR>(slot_in + o_r, pitch, r + at);
         }
-        if (gin != nullptr) fetch<TR>(s + o_g, pitch, gin + at);
+        if (gin != nullptr) fetch<TR>(slot_in + o_g, pitch, gin + at);
       }
       ahead = next_row(ahead);
     }
     cp_commit();
-    if (++slot_in == a.stages) slot_in = 0;
+    slot_in += stage_bytes;
+    if (slot_in == ring_end) slot_in = mine_a;
   };
-  float s1[8], p1[8], s2[BIAS ? 8 : 1], p2[BIAS ? 8 : 1];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    s1[i] = p1[i] = 0.f;
-    if constexpr (BIAS) s2[i] = p2[i] = 0.f;
-  }
+  F8 s1 = zero8f(), p1 = zero8f(), s2 = zero8f(), p2 = zero8f();
   // sum of v over the row groups, in group order (in group 0's threads)
-  auto join = [&](float* v) {
+  auto join = [&](F8& v) {
     if (a.R == 1) return;
     __syncthreads();
-    float* at = swap + (g * a.tpr + vec) * 8;
-    store8(at, v);
+    store_f8(swap + (g * a.tpr + vec) * 8, v);
     __syncthreads();
-    if (g == 0) {
-      for (int k = 1; k < a.R; ++k) {
-        float o[8];
-        load8(swap + (k * a.tpr + vec) * 8, o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += o[i];
-      }
-    }
+    if (g == 0)
+      for (int k = 1; k < a.R; ++k) v = add8(v, load_f8(swap + (k * a.tpr + vec) * 8));
   };
 
   const float4* stats = reinterpret_cast<const float4*>(a.stats_in);
   float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
   if (ahead < row1) st_next = stats[ahead];
   for (int i = 0; i < a.stages - 1; ++i) issue();
-  int slot = 0;
+  // idle threads of a row's last warp hold zeros in both vectors and in
+  // every tensor they weight, so they add nothing to the row's sums
+  keep(v_pre, pitch, active && a.w_pre != nullptr ? load_f8(a.w_pre + c0) : zero8f());
+  const uint8_t* slot = mine;
   for (int seg0 = row0; seg0 < row1;) {
     const int seg1 = seg_end(seg0);
     const float* gate = a.gate_len > 0 ? a.gate + (int64_t)(seg0 / a.gate_len) * a.D + c0 : nullptr;
     if (y != nullptr) {
-      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      F8 w = zero8f();
       if (active) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = a.alpha;
-        float o[8];
-        if (gate != nullptr) {
-          load8(gate, o);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] *= o[i];
-        }
-        if (a.w_post != nullptr) {
-          load8(a.w_post + c0, o);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] *= o[i];
-        }
+        w = add8(w, pack2(a.alpha, a.alpha));
+        if (gate != nullptr) w = mul8(w, load_f8(gate));
+        if (a.w_post != nullptr) w = mul8(w, load_f8(a.w_post + c0));
       }
-      keep(v_post, w);
+      keep(v_post, pitch, w);
     }
     for (int t = seg0 + g; t < seg1; t += a.R) {
       issue();
@@ -425,170 +484,108 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
       const int tn = next_row(t);
       if (tn < row1) st_next = stats[tn];
       const int64_t at = (int64_t)t * a.D + c0;
-      const uint8_t* from = mine + slot * stage_bytes;
-      if (a.stages > 0) {
-        cp_wait(a.stages - 1);
-        if (++slot == a.stages) slot = 0;
-      }
+      if (a.stages > 0) cp_wait(a.stages - 1);
       // this thread's columns of one tensor (rows that fit no ring: from
       // global memory)
-      auto get = [&](auto* base, int off, float* f) {
+      auto get = [&](auto* base, int off) -> F8 {
         using T = std::remove_cv_t<std::remove_pointer_t<decltype(base)>>;
-        if (a.stages > 0) take<T>(from + off, pitch, f);
-        else load8(base + at, f);
+        if (!active) return zero8f();
+        return a.stages > 0 ? take<T>(slot + off, pitch) : load_f8(base + at);
       };
-      float d[8];
+      F8 d;
       if (dx != nullptr) {
-        float u[8], h[8], w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = h[i] = 0.f;
-        if (active) {
-          get(dx, o_dx, u);
-          get(r, o_r, h);
-        }
-        take<float>(v_pre, pitch, w);
-        float q1 = 0.f, q2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[i] = (h[i] - st.z) * st.w;
-          p1[i] = fmaf(u[i], h[i], p1[i]);
-          if constexpr (BIAS) p2[i] += u[i];
-          u[i] *= w[i];
-          q1 = fmaf(u[i], h[i], q1);
-        }
-        float m2 = 0.f;
-        if (a.layer) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q2 += u[i];
-          const float2 q = sum(q1, q2);
-          q1 = q.x;
-          m2 = q.y * a.inv_d;
+        F8 u = get(dx, o_dx);
+        const float c = -st.z * st.w;
+        const F8 h = fma8(get(r, o_r), pack2(st.w, st.w), pack2(c, c));
+        p1 = fma8(u, h, p1);
+        if (GENERAL) p2 = add8(p2, u);
+        u = mul8(u, take<float>(v_pre, pitch));
+        float m1;
+        if (GENERAL && a.layer) {
+          const float2 q = sum(dot8(u, h), sum8(u));
+          m1 = -q.x * a.inv_d;
+          const float m2 = -q.y * a.inv_d;
+          u = add8(u, pack2(m2, m2));
         } else {
-          q1 = sum(q1);
+          m1 = -sum(dot8(u, h)) * a.inv_d;
         }
-        const float m1 = -q1 * a.inv_d;
         // rstd (u - m2 - h m1) + dr_out
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = fmaf(h[i], m1, u[i] - m2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = 0.f;
-        if (gin != nullptr && active) get(gin, o_g, d);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = fmaf(st.w, u[i], d[i]);
+        u = fma8(h, pack2(m1, m1), u);
+        d = gin != nullptr ? get(gin, o_g) : zero8f();
+        d = fma8(u, pack2(st.w, st.w), d);
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = 0.f;
-        if (gin != nullptr && active) get(gin, o_g, d);
+        d = gin != nullptr ? get(gin, o_g) : zero8f();
       }
-      if (active) store8(static_cast<TR*>(a.dr) + at, d);
+      if (active) store_f8(static_cast<TR*>(a.dr) + at, d);
       if (y != nullptr) {
-        float yv[8], e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) yv[i] = 0.f;
-        if (active) get(y, 0, yv);
-        take<float>(v_post, pitch, e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          yv[i] = (yv[i] - st.x) * st.y;
-          s1[i] = fmaf(d[i], yv[i], s1[i]);
-          if constexpr (BIAS) s2[i] += d[i];
-          e[i] *= d[i];
-        }
+        const float c = -st.x * st.y;
+        const F8 yh = fma8(get(y, 0), pack2(st.y, st.y), pack2(c, c));
+        s1 = fma8(d, yh, s1);
+        if (GENERAL) s2 = add8(s2, d);
+        F8 e = mul8(d, take<float>(v_post, pitch));
         if (a.w_post != nullptr) {
-          float q1 = 0.f, q2 = 0.f, m2 = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q1 = fmaf(e[i], yv[i], q1);
-          if (a.layer) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q2 += e[i];
-            const float2 q = sum(q1, q2);
-            q1 = q.x;
-            m2 = q.y * a.inv_d;
+          float m1;
+          if (GENERAL && a.layer) {
+            const float2 q = sum(dot8(e, yh), sum8(e));
+            m1 = -q.x * a.inv_d;
+            const float m2 = -q.y * a.inv_d;
+            e = add8(e, pack2(m2, m2));
           } else {
-            q1 = sum(q1);
+            m1 = -sum(dot8(e, yh)) * a.inv_d;
           }
-          const float m1 = -q1 * a.inv_d;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = st.y * fmaf(yv[i], m1, e[i] - m2);
+          e = mul8(fma8(yh, pack2(m1, m1), e), pack2(st.y, st.y));
         }
-        if (active) store8(static_cast<TA*>(a.dy) + at, e);
+        if (active) store_f8(static_cast<TA*>(a.dy) + at, e);
       }
+      slot += stage_bytes;
+      if (smem_addr(slot) == ring_end) slot = mine;
     }
-    if (a.several) {
+    if constexpr (SEVERAL) {
       join(s1);
-      if constexpr (BIAS) join(s2);
+      if (GENERAL) join(s2);
       if (g == 0 && active) {
-        float wg[8];
-        load8(gate, wg);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w_sum[c0 + i] = fmaf(wg[i], s1[i], w_sum[c0 + i]);
-          if constexpr (BIAS) w_sum[a.D + c0 + i] = fmaf(wg[i], s2[i], w_sum[a.D + c0 + i]);
-        }
+        const F8 wg = load_f8(gate);
+        store_f8(w_sum + c0, fma8(wg, s1, load_f8(w_sum + c0)));
+        if (GENERAL) store_f8(w_sum + a.D + c0, fma8(wg, s2, load_f8(w_sum + a.D + c0)));
         const int gr = seg0 / L;
         const int64_t gs = (int64_t)gr * L, ge = min((int64_t)a.T, gs + L);
         if (gs >= row0 && ge <= row1) {
           if (a.dgate != nullptr) {
-            float w[8], o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = s1[i];
-            if (a.w_post != nullptr) {
-              load8(a.w_post + c0, w);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] *= w[i];
-            }
-            if constexpr (BIAS) {
-              if (a.b_post != nullptr) {
-                load8(a.b_post + c0, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(w[i], s2[i], o[i]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] *= a.alpha;
-            store8(a.dgate + (int64_t)gr * a.D + c0, o);
+            F8 o = s1;
+            if (a.w_post != nullptr) o = mul8(o, load_f8(a.w_post + c0));
+            if (GENERAL && a.b_post != nullptr) o = fma8(load_f8(a.b_post + c0), s2, o);
+            store_f8(a.dgate + (int64_t)gr * a.D + c0, mul8(o, pack2(a.alpha, a.alpha)));
           }
         } else {
           const bool head = gs < row0;
-          store8(part + (head ? S1H : S1T) * arr, s1);
-          if constexpr (BIAS) store8(part + (head ? S2H : S2T) * arr, s2);
+          store_f8(part + (head ? S1H : S1T) * arr, s1);
+          if (GENERAL) store_f8(part + (head ? S2H : S2T) * arr, s2);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s1[i] = 0.f;
-        if constexpr (BIAS) s2[i] = 0.f;
-      }
+      s1 = s2 = zero8f();
     }
     seg0 = seg1;
   }
   cp_wait(0);
-  if (!a.several && a.y != nullptr) {
+  if (!SEVERAL && a.y != nullptr) {
     join(s1);
-    if (g == 0 && active) store8(part + S1H * arr, s1);
-    if constexpr (BIAS) {
+    if (g == 0 && active) store_f8(part + S1H * arr, s1);
+    if (GENERAL) {
       join(s2);
-      if (g == 0 && active) store8(part + S2H * arr, s2);
+      if (g == 0 && active) store_f8(part + S2H * arr, s2);
     }
   }
   if (a.dx != nullptr) {
     join(p1);
-    if (g == 0 && active) store8(part + P1 * arr, p1);
-    if constexpr (BIAS) {
+    if (g == 0 && active) store_f8(part + P1 * arr, p1);
+    if (GENERAL) {
       join(p2);
-      if (g == 0 && active) store8(part + P2 * arr, p2);
+      if (g == 0 && active) store_f8(part + P2 * arr, p2);
     }
   }
-  if (a.several && g == 0 && active) {
-    float o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = w_sum[c0 + i];
-    store8(part + W1 * arr, o);
-    if constexpr (BIAS) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = w_sum[a.D + c0 + i];
-      store8(part + W2 * arr, o);
-    }
+  if (SEVERAL && g == 0 && active) {
+    store_f8(part + W1 * arr, load_f8(w_sum + c0));
+    if (GENERAL) store_f8(part + W2 * arr, load_f8(w_sum + a.D + c0));
   }
 }
 
@@ -729,41 +726,59 @@ bool any_misaligned(P... p) {
   return (host::misaligned(p, 16) || ...);
 }
 
-template <typename TA, typename TR>
-int forward(NormArgs a, cudaStream_t s) {
-  auto k = block_norm_kernel<TA, TR>;
-  a.R = row_groups(a.tpr, 256);
-  const int sms = host::sm_count();
-  a.R = (int)std::max<int64_t>(1, std::min<int64_t>(a.R, host::ceil_div(a.T, sms)));
-  const int threads = a.R * a.tpr;
-  const size_t stage = (size_t)(kPiece<TA> + kPiece<TR>) * threads;
-  const int per_sm = std::max(1, 2048 / threads);
-  // the ring holds what a CTA's share of shared memory takes, 3 stages at most
-  a.stages = (int)std::max<size_t>(1, std::min<size_t>(3, kSmemLimit / per_sm / stage));
-  const size_t smem = a.stages * stage;
-  MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit - 9 * 1024));
-  const int64_t want = host::ceil_div(a.T, a.R);
-  const int grid = (int)std::min<int64_t>(want, (int64_t)sms * per_sm);
-  return host::launch("block_norm", k, grid, threads, smem, s, 1, a);
+// Calls f with the template's truth values for two run-time ones.
+template <typename F>
+int with_flags(bool p, bool q, F f) {
+  if (p) return q ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  return q ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
 }
 
-template <typename TA, typename TR, bool BIAS>
-int backward(NormArgs a, int P, SumArgs& sum, cudaStream_t s) {
-  auto k = block_norm_bwd_kernel<TA, TR, BIAS>;
+template <typename TA, typename TR>
+int forward(NormArgs a, cudaStream_t s) {
+  const int sms = host::sm_count();
+  a.R = row_groups(a.tpr, 256);
+  a.R = (int)std::max<int64_t>(1, std::min<int64_t>(a.R, host::ceil_div(a.T, sms)));
   const int threads = a.R * a.tpr;
+  const bool bias = a.b_post != nullptr || a.b_pre != nullptr;
+  const size_t stage = (size_t)(kPiece<TA> + kPiece<TR>) * threads;
+  const size_t fixed = (size_t)threads * 32 * (bias ? 4 : 2);
+  // 64 registers a thread: 1024 threads of an SM
+  const int per_sm = std::max(1, 1024 / threads);
+  const size_t room = (kSmemLimit + 1024) / per_sm - 9 * 1024;
+  a.stages = (int)std::max<size_t>(1, std::min<size_t>(4, (room - std::min(room, fixed)) / stage));
+  const size_t smem = a.stages * stage + fixed;
+  const int grid = (int)std::min<int64_t>(host::ceil_div(a.T, a.R), (int64_t)sms * per_sm);
+  return with_flags(bias, a.D % 256 == 0, [&](auto b, auto f) {
+    auto k = block_norm_kernel<TA, TR, decltype(b)::value, decltype(f)::value>;
+    MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem));
+    return host::launch("block_norm", k, grid, threads, smem, s, 1, a);
+  });
+}
+
+template <typename TA, typename TR>
+int backward(NormArgs a, int P, bool bias, SumArgs& sum, cudaStream_t s) {
+  const int threads = a.R * a.tpr;
+  const bool general = bias || a.layer;
   const size_t stage = 2 * (size_t)(kPiece<TA> + kPiece<TR>) * threads;
-  const size_t fixed = (size_t)threads * 64 + (a.several ? (BIAS ? 2 : 1) * (size_t)a.D * 4 : 0) +
+  const size_t fixed = (size_t)threads * 64 + (a.several ? (general ? 2 : 1) * (size_t)a.D * 4 : 0) +
                        (a.R > 1 ? (size_t)threads * 32 : 0);
   // two CTAs an SM share its shared memory (8 KB static and 1 KB of the
   // system's each)
-  const size_t room = (threads > 512 ? kSmemLimit : kSmemLimit / 2) - 9 * 1024 - fixed;
+  const size_t room = (threads > 512 ? kSmemLimit + 1024 : (kSmemLimit + 1024) / 2) - 9 * 1024 - fixed;
   // a ring of one stage would overlap nothing: rows too long for two (wide
   // fp32 rows) are read where they are used
   a.stages = (int)std::min<size_t>(3, room / stage);
   if (a.stages < 2) a.stages = 0;
   const size_t smem = a.stages * stage + fixed;
-  MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit - 9 * 1024));
-  MOE_HTRY(host::launch("block_norm_bwd", k, P, threads, smem, s, 1, a));
+  auto go = [&](auto k) {
+    MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem));
+    return host::launch("block_norm_bwd", k, P, threads, smem, s, 1, a);
+  };
+  MOE_HTRY(with_flags(general, a.several != 0, [&](auto ge, auto se) {
+    constexpr bool G = decltype(ge)::value, S = decltype(se)::value;
+    return a.D % 256 == 0 ? go(block_norm_bwd_kernel<TA, TR, G, S, true>)
+                          : go(block_norm_bwd_kernel<TA, TR, G, S, false>);
+  }));
   sum.n = a;
   sum.P = P;
   // dgate of the gate rows that CTAs cut: by gate row where there are fewer
@@ -841,14 +856,9 @@ int moe_block_norm_backward(const moe_norm_config_t* c, const void* r_out, const
   int P = 0;
   bwd_shape(c, &P, &a.R);
   const bool bias = db_post != nullptr || db_pre != nullptr || (dgate != nullptr && b_post != nullptr);
-  auto go = [&](auto ta, auto tr) {
-    using TA = decltype(ta);
-    using TR = decltype(tr);
-    return bias ? backward<TA, TR, true>(a, P, sum, s) : backward<TA, TR, false>(a, P, sum, s);
-  };
-  if (c->dtype == MOE_FP32) return go(float{}, float{});
-  if (c->resid == MOE_FP32) return go(__nv_bfloat16{}, float{});
-  return go(__nv_bfloat16{}, __nv_bfloat16{});
+  if (c->dtype == MOE_FP32) return backward<float, float>(a, P, bias, sum, s);
+  if (c->resid == MOE_FP32) return backward<__nv_bfloat16, float>(a, P, bias, sum, s);
+  return backward<__nv_bfloat16, __nv_bfloat16>(a, P, bias, sum, s);
 }
 
 }  // extern "C"

@@ -4,13 +4,19 @@
 //   p' = p - lr (m'/c1 / (sqrt(v'/c2) + eps) + wd p),  c_i = 1 - b_i^t
 //
 // Every element is independent, so the step is bound by DRAM: parameter,
-// gradient and states are read and written once.  A chunk of 2048 elements
-// goes to a block of 8 warps, 8 consecutive elements to a thread; a warp
-// then holds exactly one 256-element block of the 8-bit states, whose new
-// scale is one warp-wide maximum (redux.sync on the bits of the magnitudes,
-// which order as the values do, NaN on top), and no value leaves registers.
-// The tensors' descriptors are kernel arguments: nothing is copied to the
-// device, and a chunk finds its tensor by bisection in constant memory.
+// gradient and states are read and written once (10 bytes an element with
+// bf16 weights and 8-bit states, 22 with 32-bit ones).  At that rate an
+// element may take about 55 instructions, so the arithmetic runs on packed
+// pairs, with the hardware's approximate root and reciprocal (2^-22
+// relative, far inside the update's own rounding; squares below 2^-126 count
+// as zero).  A chunk of 4096 elements goes to a block of 8 warps, twice 8
+// consecutive elements to a thread, all loads first; a warp then holds
+// exactly two 256-element blocks of the 8-bit states, whose new scales are
+// warp-wide maxima, and no value leaves registers.  The tensors' descriptors
+// are kernel arguments: nothing is copied to the device, and a chunk finds
+// its tensor by bisection in constant memory.  Tensors of one state kind
+// share a launch; parameter, gradient and master types select straight-line
+// code per chunk.
 //
 // 8-bit states are e4m3 (4 exponent bits, half a step is 2^-4 of the value)
 // with the largest of a block at 448.  The second moment is kept as its
@@ -20,17 +26,21 @@
 // divide by.
 #include <cuda_fp8.h>
 #include <cmath>
+#include <type_traits>
 
+#include "f32x2.cuh"
 #include "host.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = kThreads * 8;
+constexpr int kTurn = kThreads * 8;      // elements of a block's turn
+constexpr int kTurns = 2;                // turns of a chunk
+constexpr int kChunk = kTurn * kTurns;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kE4m3Least = 0.001953125f;        // 2^-9, the smallest positive e4m3
-constexpr unsigned kStateMinBits = 0x0d800000u;   // 2^-100: blocks below hold zeros
+constexpr float kStateMin = 7.8886091e-31f;       // 2^-100: blocks below hold zeros
 
 struct Tensor {
   void* p;
@@ -52,86 +62,243 @@ struct Args {
   const float *lr_dev, *grad_scale;
 };
 
-__device__ __forceinline__ void load_any(const void* base, int64_t i, int64_t n, bool bf16,
-                                         bool whole, float* f) {
-  if (bf16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + i;
-    if (whole) { load8(p, f); return; }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = i + k < n ? __bfloat162float(p[k]) : 0.f;
-  } else {
-    const float* p = static_cast<const float*>(base) + i;
-    if (whole) { load8(p, f); return; }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = i + k < n ? p[k] : 0.f;
-  }
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
-__device__ __forceinline__ void store_any(void* base, int64_t i, int64_t n, bool bf16, bool whole,
-                                          const float* f) {
-  if (bf16) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + i;
-    if (whole) { store8(p, f); return; }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i + k < n) p[k] = __float2bfloat16_rn(f[k]);
-  } else {
-    float* p = static_cast<float*>(base) + i;
-    if (whole) { store8(p, f); return; }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i + k < n) p[k] = f[k];
-  }
+__device__ __forceinline__ float root_of(float v) {
+  float d;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
 }
-__device__ __forceinline__ void load_fp8(const void* base, int64_t i, int64_t n, bool whole,
-                                         float scale, float* f) {
-  const uint8_t* p = static_cast<const uint8_t*>(base) + i;
-  union { uint2 u; __nv_fp8x2_storage_t q[4]; uint8_t b[8]; } w;
-  if (whole) {
-    w.u = *reinterpret_cast<const uint2*>(p);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w.b[k] = i + k < n ? p[k] : 0;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(w.q[k], __NV_E4M3)));
-    f[2 * k] = v.x * scale;
-    f[2 * k + 1] = v.y * scale;
-  }
+__device__ __forceinline__ float recip(float v) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
 }
-__device__ __forceinline__ void store_fp8(void* base, int64_t i, int64_t n, bool whole,
-                                          const float* f) {
-  uint8_t* p = static_cast<uint8_t*>(base) + i;
-  union { uint2 u; __nv_fp8x2_storage_t q[4]; uint8_t b[8]; } w;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    w.q[k] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE,
-                                      __NV_E4M3);
-  if (whole) {
-    *reinterpret_cast<uint2*>(p) = w.u;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i + k < n) p[k] = w.b[k];
-  }
+__device__ __forceinline__ F8 widen_fp8(const uint2& u) {
+  auto two = [](uint32_t w) {
+    const float2 f = __half22float2(__half2(
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3)));
+    return pack2(f.x, f.y);
+  };
+  return F8{{two(u.x), two(u.x >> 16), two(u.y), two(u.y >> 16)}};
 }
-// Scale of a block from its largest magnitude's bits, and what its values
-// are multiplied by before rounding.  Not finite: everything becomes NaN.
-__device__ __forceinline__ float2 block_scale(unsigned bits) {
-  if (bits >= 0x7f800000u) return make_float2(__int_as_float(0x7fffffff), 0.f);
-  if (bits < kStateMinBits) return make_float2(0.f, 0.f);
-  const float big = __uint_as_float(bits);
-  return make_float2(big / kE4m3Max, kE4m3Max / big);
+__device__ __forceinline__ uint2 narrow_fp8(const F8& a) {
+  auto two = [](uint64_t v) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(unpack2(v), __NV_SATFINITE, __NV_E4M3);
+  };
+  return make_uint2(two(a.p[0]) | (two(a.p[1]) << 16), two(a.p[2]) | (two(a.p[3]) << 16));
 }
 
+// Eight elements of a tensor as they lie in memory.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int64_t n) {
+    uint16_t b[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = k < n ? __bfloat16_as_ushort(p[k]) : 0;
+    u = make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16,
+                   b[4] | (uint32_t)b[5] << 16, b[6] | (uint32_t)b[7] << 16);
+  }
+  __device__ __forceinline__ F8 wide() const { return widen8(u); }
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void load(const float* p, int64_t n) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = k < n ? p[k] : 0.f;
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  __device__ __forceinline__ F8 wide() const { return f8_of(a, b); }
+};
+template <> struct Raw<uint8_t> {      // e4m3
+  uint2 u;
+  __device__ __forceinline__ void load(const uint8_t* p) { u = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void load(const uint8_t* p, int64_t n) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) w[k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
+    u = make_uint2(w[0], w[1]);
+  }
+  __device__ __forceinline__ F8 wide() const { return widen_fp8(u); }
+};
+// The first n of eight values.
+__device__ __forceinline__ void store_part(float* p, const F8& a, int64_t n) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2(a.p[k]);
+    if (2 * k < n) p[2 * k] = f.x;
+    if (2 * k + 1 < n) p[2 * k + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store_part(__nv_bfloat16* p, const F8& a, int64_t n) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2(a.p[k]);
+    if (2 * k < n) p[2 * k] = __float2bfloat16_rn(f.x);
+    if (2 * k + 1 < n) p[2 * k + 1] = __float2bfloat16_rn(f.y);
+  }
+}
+__device__ __forceinline__ void store_fp8(uint8_t* p, const uint2& u, bool whole, int64_t n) {
+  if (whole) {
+    *reinterpret_cast<uint2*>(p) = u;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) p[k] = (uint8_t)((k < 4 ? u.x : u.y) >> (8 * (k & 3)));
+}
+// Scale of a block from its largest magnitude, and what its values are
+// multiplied by before rounding.  Not finite: everything becomes NaN.
+__device__ __forceinline__ float2 block_scale(float big) {
+  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 16));
+  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 8));
+  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 4));
+  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
+  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  if (!(big < __int_as_float(0x7f800000))) return make_float2(__int_as_float(0x7fffffff), 0.f);
+  if (big < kStateMin) return make_float2(0.f, 0.f);
+  return make_float2(big * (1.0f / kE4m3Max), kE4m3Max / big);
+}
+__device__ __forceinline__ float biggest(const F8& a) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2(a.p[k]);
+    m = max_nan(m, max_nan(fabsf(f.x), fabsf(f.y)));
+  }
+  return m;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
+
+struct Step {           // one step's values, the same for all elements
+  float gs, lr, ic1, ic2;
+};
+
+// One chunk of tensor t: TP, TG the types of parameter and gradient; MASTER:
+// the parameter is rounded from an fp32 copy.
+template <bool FP8, typename TP, typename TG, bool MASTER>
+__device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_t i0,
+                                          const Step& st) {
+  using TS = typename std::conditional<FP8, uint8_t, float>::type;
+  using TW = typename std::conditional<MASTER, float, TP>::type;
+  const TG* gp = static_cast<const TG*>(t.g);
+  TW* wp = MASTER ? reinterpret_cast<TW*>(t.master) : static_cast<TW*>(t.p);
+  TS *mp = static_cast<TS*>(t.m), *vp = static_cast<TS*>(t.v);
+  const int64_t n = t.n;
+  Raw<TG> rg[kTurns];
+  Raw<TW> rw[kTurns];
+  Raw<TS> rm[kTurns], rv[kTurns];
+  float ms[kTurns], vs[kTurns];
+  bool whole[kTurns];
+  int64_t left[kTurns];       // elements from this thread's first on (may be negative)
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k) {
+    const int64_t i = i0 + k * kTurn;
+    left[k] = n - i;
+    whole[k] = t.wide && left[k] >= 8;
+    if (whole[k]) {
+      rg[k].load(gp + i);
+      rw[k].load(wp + i);
+      rm[k].load(mp + i);
+      rv[k].load(vp + i);
+    } else {
+      rg[k].load(gp + i, left[k]);
+      rw[k].load(wp + i, left[k]);
+      rm[k].load(mp + i, left[k]);
+      rv[k].load(vp + i, left[k]);
+    }
+    if constexpr (FP8) {
+      ms[k] = left[k] > 0 ? t.ms[i / MOE_ADAMW_BLOCK] : 0.f;
+      vs[k] = left[k] > 0 ? t.vs[i / MOE_ADAMW_BLOCK] : 0.f;
+    }
+  }
+  const uint64_t lr = both(-st.lr * t.lr_mult), wd = both(t.decay ? a.wd : 0.f);
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k) {
+    const int64_t i = i0 + k * kTurn;
+    const F8 g = mul8(rg[k].wide(), both(st.gs));
+    F8 m = rm[k].wide(), v = rv[k].wide();
+    if constexpr (FP8) {
+      m = mul8(m, both(ms[k]));
+      v = mul8(v, both(vs[k]));
+      v = mul8(v, v);
+    }
+    m = fma8(m, both(a.b1), mul8(g, both(a.omb1)));
+    v = fma8(v, both(a.b2), mul8(mul8(g, both(a.omb2)), g));
+    F8 root, den;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2(v.p[j]);
+      root.p[j] = pack2(root_of(f.x), root_of(f.y));
+    }
+    den = fma8(root, both(st.ic2), both(a.eps));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2(den.p[j]);
+      den.p[j] = pack2(recip(f.x), recip(f.y));
+    }
+    const F8 p = rw[k].wide();
+    const F8 up = fma8(p, wd, mul8(mul8(m, both(st.ic1)), den));
+    const F8 w = fma8(up, lr, p);
+    TP* pp = static_cast<TP*>(t.p);
+    if (whole[k]) {
+      store_f8(pp + i, w);
+      if (MASTER) store_f8(wp + i, w);
+    } else {
+      store_part(pp + i, w, left[k]);
+      if (MASTER) store_part(wp + i, w, left[k]);
+    }
+    if constexpr (FP8) {
+      // elements behind the tensor's end were loaded as zeros and stay zeros
+      const float2 sm = block_scale(biggest(m)), sv = block_scale(biggest(root));
+      m = mul8(m, both(sm.y));
+      root = mul8(root, both(sv.y));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2(root.p[j]);
+        root.p[j] = pack2(f.x > 0.f ? fmaxf(f.x, kE4m3Least) : f.x,
+                          f.y > 0.f ? fmaxf(f.y, kE4m3Least) : f.y);
+      }
+      store_fp8(mp + i, narrow_fp8(m), whole[k], left[k]);
+      store_fp8(vp + i, narrow_fp8(root), whole[k], left[k]);
+      if ((threadIdx.x & 31) == 0 && left[k] > 0) {
+        t.ms[i / MOE_ADAMW_BLOCK] = sm.x;
+        t.vs[i / MOE_ADAMW_BLOCK] = sv.x;
+      }
+    } else if (whole[k]) {
+      store_f8(mp + i, m);
+      store_f8(vp + i, v);
+    } else {
+      store_part(mp + i, m, left[k]);
+      store_part(vp + i, v, left[k]);
+    }
+  }
+}
+
+template <bool FP8>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Args a) {
   pdl_begin();
   const int step = a.step[0] + 1;
+  Step st;
   // 1 - b^t without cancellation
-  const float ic1 = 1.0f / -expm1f((float)step * a.lb1);
-  const float ic2 = rsqrtf(-expm1f((float)step * a.lb2));
-  const float gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-  const float lr0 = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+  st.ic1 = 1.0f / -expm1f((float)step * a.lb1);
+  st.ic2 = rsqrtf(-expm1f((float)step * a.lb2));
+  st.gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+  st.lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
   const int64_t total = a.first[a.n];
   for (int64_t chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
     int lo = 0, hi = a.n;                  // the last tensor with first <= chunk
@@ -140,62 +307,17 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       if (a.first[mid] <= chunk) lo = mid; else hi = mid;
     }
     const Tensor& t = a.t[lo];
-    const int64_t n = t.n;
-    const int64_t i = (chunk - a.first[lo]) * kChunk + threadIdx.x * 8;
-    const bool whole = t.wide && i + 8 <= n;
-    const float lr = lr0 * t.lr_mult, wd = t.decay ? a.wd : 0.f;
-    float p[8], g[8], m[8], v[8];
-    const int64_t blk = i / MOE_ADAMW_BLOCK;
-    const bool some = i < n;
-    load_any(t.g, i, n, t.g_bf16, whole, g);
-    if (t.master != nullptr) load_any(t.master, i, n, false, whole, p);
-    else load_any(t.p, i, n, t.p_bf16, whole, p);
-    if (t.fp8) {
-      load_fp8(t.m, i, n, whole, some ? t.ms[blk] : 0.f, m);
-      load_fp8(t.v, i, n, whole, some ? t.vs[blk] : 0.f, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= v[k];
+    const int64_t i0 = (chunk - a.first[lo]) * kChunk + threadIdx.x * 8;
+    using bf16 = __nv_bfloat16;
+    if (t.master != nullptr) {
+      if (t.g_bf16) run_chunk<FP8, bf16, bf16, true>(a, t, i0, st);
+      else run_chunk<FP8, bf16, float, true>(a, t, i0, st);
+    } else if (t.p_bf16) {
+      if (t.g_bf16) run_chunk<FP8, bf16, bf16, false>(a, t, i0, st);
+      else run_chunk<FP8, bf16, float, false>(a, t, i0, st);
     } else {
-      load_any(t.m, i, n, false, whole, m);
-      load_any(t.v, i, n, false, whole, v);
-    }
-    float root[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float gk = g[k] * gs;
-      m[k] = fmaf(a.b1, m[k], a.omb1 * gk);
-      v[k] = fmaf(a.b2, v[k], a.omb2 * gk * gk);
-      root[k] = sqrtf(v[k]);
-      const float up = (m[k] * ic1) / fmaf(root[k], ic2, a.eps);
-      p[k] = fmaf(-lr, fmaf(wd, p[k], up), p[k]);
-    }
-    store_any(t.p, i, n, t.p_bf16, whole, p);
-    if (t.master != nullptr) store_any(t.master, i, n, false, whole, p);
-    if (t.fp8) {
-      unsigned bm = 0, bv = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (!whole && i + k >= n) continue;
-        bm = max(bm, __float_as_uint(m[k]) & 0x7fffffffu);
-        bv = max(bv, __float_as_uint(root[k]) & 0x7fffffffu);
-      }
-      const float2 sm = block_scale(__reduce_max_sync(0xffffffffu, bm));
-      const float2 sv = block_scale(__reduce_max_sync(0xffffffffu, bv));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] *= sm.y;
-        const float s = root[k] * sv.y;
-        root[k] = s > 0.f && s < kE4m3Least ? kE4m3Least : s;
-      }
-      store_fp8(t.m, i, n, whole, m);
-      store_fp8(t.v, i, n, whole, root);
-      if ((threadIdx.x & 31) == 0 && some) {
-        t.ms[blk] = sm.x;
-        t.vs[blk] = sv.x;
-      }
-    } else {
-      store_any(t.m, i, n, false, whole, m);
-      store_any(t.v, i, n, false, whole, v);
+      if (t.g_bf16) run_chunk<FP8, float, bf16, false>(a, t, i0, st);
+      else run_chunk<FP8, float, float, false>(a, t, i0, st);
     }
   }
   // the block that comes last counts the step: all have read the old count
@@ -260,22 +382,41 @@ extern "C" int moe_adamw(const moe_adamw_config_t* c, const moe_adamw_tensor_t* 
   a.b2 = (float)c->beta2; a.omb2 = (float)(1.0 - c->beta2); a.lb2 = (float)std::log(c->beta2);
   a.eps = (float)c->eps; a.wd = (float)c->weight_decay;
   a.step = step; a.lr_dev = lr; a.grad_scale = grad_scale;
-  int i = 0;
-  do {
+  // launches of up to MOE_ADAMW_MAX tensors of one state kind; the last one
+  // counts the step (a list without elements still is a step)
+  const int64_t per_sm = 4;
+  auto fill = [&](int from, bool fp8) {    // next tensors of a kind; where to go on
     a.n = 0;
     int64_t chunks = 0;
+    int i = from;
     for (; i < n_tensors && a.n < MOE_ADAMW_MAX; ++i) {
-      if (tensors[i].n == 0) continue;
+      if (tensors[i].n == 0 || (tensors[i].state == MOE_STATE_FP8) != fp8) continue;
       describe(tensors[i], &a.t[a.n]);
       a.first[a.n++] = chunks;
       chunks += host::ceil_div(tensors[i].n, kChunk);
     }
     a.first[a.n] = chunks;
-    while (i < n_tensors && tensors[i].n == 0) ++i;
-    a.last = i == n_tensors;
-    const int grid = (int)std::max<int64_t>(
-        1, std::min<int64_t>(chunks, (int64_t)host::sm_count() * (2048 / kThreads)));
-    MOE_HTRY(host::launch("adamw", adamw_kernel, grid, kThreads, 0, s, 1, a));
-  } while (i < n_tensors);
+    return i;
+  };
+  auto more = [&](int from, bool fp8) {
+    for (int i = from; i < n_tensors; ++i)
+      if (tensors[i].n != 0 && (tensors[i].state == MOE_STATE_FP8) == fp8) return true;
+    return false;
+  };
+  for (int kind = 0; kind < 2; ++kind) {
+    const bool fp8 = kind == 1;
+    int i = 0;
+    // the 8-bit kind comes last and ends the step, with nothing to do if
+    // there is none of either
+    while (more(i, fp8) || (fp8 && i == 0 && !more(0, false))) {
+      i = fill(i, fp8);
+      a.last = !more(i, fp8) && (fp8 || !more(0, true));
+      const int grid = (int)std::max<int64_t>(
+          1, std::min<int64_t>(a.first[a.n], (int64_t)host::sm_count() * per_sm));
+      MOE_HTRY(host::launch("adamw", fp8 ? adamw_kernel<true> : adamw_kernel<false>, grid, kThreads,
+                            0, s, 1, a));
+      if (a.last) return MOE_OK;
+    }
+  }
   return MOE_OK;
 }

@@ -9,10 +9,10 @@
 // element may take about 55 instructions, so the arithmetic runs on packed
 // pairs, with the hardware's approximate root and reciprocal (2^-22
 // relative, far inside the update's own rounding; squares below 2^-126 count
-// as zero).  A chunk of 4096 elements goes to a block of 8 warps, twice 8
-// consecutive elements to a thread, all loads first; a warp then holds
-// exactly two 256-element blocks of the 8-bit states, whose new scales are
-// warp-wide maxima, and no value leaves registers.  The tensors' descriptors
+// as zero).  A chunk of 2048 elements goes to a block of 8 warps, 8 consecutive
+// elements to a thread; a warp then holds exactly one 256-element block of
+// the 8-bit states, whose new scales are warp-wide maxima, and no value
+// leaves registers.  The tensors' descriptors
 // are kernel arguments: nothing is copied to the device, and a chunk finds
 // its tensor by bisection in constant memory.  Tensors of one state kind
 // share a launch; parameter, gradient and master types select straight-line
@@ -25,6 +25,7 @@
 // smallest positive value instead, or m / sqrt(v) would have nothing to
 // divide by.
 #include <cuda_fp8.h>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -35,9 +36,15 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTurn = kThreads * 8;      // elements of a block's turn
-constexpr int kTurns = 2;                // turns of a chunk
-constexpr int kChunk = kTurn * kTurns;
+constexpr int kChunk = kThreads * 8;
+// Blocks that an SM holds (48 and 62 registers a thread), and grids that
+// the launch asks for at most: with 32 the hardware evens out what faster
+// and slower SMs take (one grid of resident blocks measured 105.8 us on the
+// MiniMind-shaped layer's 32-bit states against 90.3, and 834 against 780 us
+// on the OLMoE-shaped layer's 8-bit ones; a block per chunk 91 and 960, its
+// own start then costs as much as the chunk).
+template <bool FP8> constexpr int kPerSm = FP8 ? 5 : 4;
+constexpr int kGrids = 32;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kE4m3Least = 0.001953125f;        // 2^-9, the smallest positive e4m3
 constexpr float kStateMin = 7.8886091e-31f;       // 2^-100: blocks below hold zeros
@@ -191,106 +198,95 @@ struct Step {           // one step's values, the same for all elements
 // One chunk of tensor t: TP, TG the types of parameter and gradient; MASTER:
 // the parameter is rounded from an fp32 copy.
 template <bool FP8, typename TP, typename TG, bool MASTER>
-__device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_t i0,
+__device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_t i,
                                           const Step& st) {
   using TS = typename std::conditional<FP8, uint8_t, float>::type;
   using TW = typename std::conditional<MASTER, float, TP>::type;
   const TG* gp = static_cast<const TG*>(t.g);
   TW* wp = MASTER ? reinterpret_cast<TW*>(t.master) : static_cast<TW*>(t.p);
   TS *mp = static_cast<TS*>(t.m), *vp = static_cast<TS*>(t.v);
-  const int64_t n = t.n;
-  Raw<TG> rg[kTurns];
-  Raw<TW> rw[kTurns];
-  Raw<TS> rm[kTurns], rv[kTurns];
-  float ms[kTurns], vs[kTurns];
-  bool whole[kTurns];
-  int64_t left[kTurns];       // elements from this thread's first on (may be negative)
-#pragma unroll
-  for (int k = 0; k < kTurns; ++k) {
-    const int64_t i = i0 + k * kTurn;
-    left[k] = n - i;
-    whole[k] = t.wide && left[k] >= 8;
-    if (whole[k]) {
-      rg[k].load(gp + i);
-      rw[k].load(wp + i);
-      rm[k].load(mp + i);
-      rv[k].load(vp + i);
-    } else {
-      rg[k].load(gp + i, left[k]);
-      rw[k].load(wp + i, left[k]);
-      rm[k].load(mp + i, left[k]);
-      rv[k].load(vp + i, left[k]);
-    }
-    if constexpr (FP8) {
-      ms[k] = left[k] > 0 ? t.ms[i / MOE_ADAMW_BLOCK] : 0.f;
-      vs[k] = left[k] > 0 ? t.vs[i / MOE_ADAMW_BLOCK] : 0.f;
-    }
+  Raw<TG> rg;
+  Raw<TW> rw;
+  Raw<TS> rm, rv;
+  float ms, vs;
+  const int64_t left = t.n - i;       // elements from this thread's first on (may be negative)
+  const bool whole = t.wide && left >= 8;
+  if (whole) {
+    rg.load(gp + i);
+    rw.load(wp + i);
+    rm.load(mp + i);
+    rv.load(vp + i);
+  } else {
+    rg.load(gp + i, left);
+    rw.load(wp + i, left);
+    rm.load(mp + i, left);
+    rv.load(vp + i, left);
+  }
+  if constexpr (FP8) {
+    ms = left > 0 ? t.ms[i / MOE_ADAMW_BLOCK] : 0.f;
+    vs = left > 0 ? t.vs[i / MOE_ADAMW_BLOCK] : 0.f;
   }
   const uint64_t lr = both(-st.lr * t.lr_mult), wd = both(t.decay ? a.wd : 0.f);
+  const F8 g = mul8(rg.wide(), both(st.gs));
+  F8 m = rm.wide(), v = rv.wide();
+  if constexpr (FP8) {
+    m = mul8(m, both(ms));
+    v = mul8(v, both(vs));
+    v = mul8(v, v);
+  }
+  m = fma8(m, both(a.b1), mul8(g, both(a.omb1)));
+  v = fma8(v, both(a.b2), mul8(mul8(g, both(a.omb2)), g));
+  F8 root, den;
 #pragma unroll
-  for (int k = 0; k < kTurns; ++k) {
-    const int64_t i = i0 + k * kTurn;
-    const F8 g = mul8(rg[k].wide(), both(st.gs));
-    F8 m = rm[k].wide(), v = rv[k].wide();
-    if constexpr (FP8) {
-      m = mul8(m, both(ms[k]));
-      v = mul8(v, both(vs[k]));
-      v = mul8(v, v);
-    }
-    m = fma8(m, both(a.b1), mul8(g, both(a.omb1)));
-    v = fma8(v, both(a.b2), mul8(mul8(g, both(a.omb2)), g));
-    F8 root, den;
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack2(v.p[j]);
+    root.p[j] = pack2(root_of(f.x), root_of(f.y));
+  }
+  den = fma8(root, both(st.ic2), both(a.eps));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack2(den.p[j]);
+    den.p[j] = pack2(recip(f.x), recip(f.y));
+  }
+  const F8 p = rw.wide();
+  const F8 up = fma8(p, wd, mul8(mul8(m, both(st.ic1)), den));
+  const F8 w = fma8(up, lr, p);
+  TP* pp = static_cast<TP*>(t.p);
+  if (whole) {
+    store_f8(pp + i, w);
+    if (MASTER) store_f8(wp + i, w);
+  } else {
+    store_part(pp + i, w, left);
+    if (MASTER) store_part(wp + i, w, left);
+  }
+  if constexpr (FP8) {
+    // elements behind the tensor's end were loaded as zeros and stay zeros
+    const float2 sm = block_scale(biggest(m)), sv = block_scale(biggest(root));
+    m = mul8(m, both(sm.y));
+    root = mul8(root, both(sv.y));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2(v.p[j]);
-      root.p[j] = pack2(root_of(f.x), root_of(f.y));
+      const float2 f = unpack2(root.p[j]);
+      root.p[j] = pack2(f.x > 0.f ? fmaxf(f.x, kE4m3Least) : f.x,
+                        f.y > 0.f ? fmaxf(f.y, kE4m3Least) : f.y);
     }
-    den = fma8(root, both(st.ic2), both(a.eps));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2(den.p[j]);
-      den.p[j] = pack2(recip(f.x), recip(f.y));
+    store_fp8(mp + i, narrow_fp8(m), whole, left);
+    store_fp8(vp + i, narrow_fp8(root), whole, left);
+    if ((threadIdx.x & 31) == 0 && left > 0) {
+      t.ms[i / MOE_ADAMW_BLOCK] = sm.x;
+      t.vs[i / MOE_ADAMW_BLOCK] = sv.x;
     }
-    const F8 p = rw[k].wide();
-    const F8 up = fma8(p, wd, mul8(mul8(m, both(st.ic1)), den));
-    const F8 w = fma8(up, lr, p);
-    TP* pp = static_cast<TP*>(t.p);
-    if (whole[k]) {
-      store_f8(pp + i, w);
-      if (MASTER) store_f8(wp + i, w);
-    } else {
-      store_part(pp + i, w, left[k]);
-      if (MASTER) store_part(wp + i, w, left[k]);
-    }
-    if constexpr (FP8) {
-      // elements behind the tensor's end were loaded as zeros and stay zeros
-      const float2 sm = block_scale(biggest(m)), sv = block_scale(biggest(root));
-      m = mul8(m, both(sm.y));
-      root = mul8(root, both(sv.y));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2(root.p[j]);
-        root.p[j] = pack2(f.x > 0.f ? fmaxf(f.x, kE4m3Least) : f.x,
-                          f.y > 0.f ? fmaxf(f.y, kE4m3Least) : f.y);
-      }
-      store_fp8(mp + i, narrow_fp8(m), whole[k], left[k]);
-      store_fp8(vp + i, narrow_fp8(root), whole[k], left[k]);
-      if ((threadIdx.x & 31) == 0 && left[k] > 0) {
-        t.ms[i / MOE_ADAMW_BLOCK] = sm.x;
-        t.vs[i / MOE_ADAMW_BLOCK] = sv.x;
-      }
-    } else if (whole[k]) {
-      store_f8(mp + i, m);
-      store_f8(vp + i, v);
-    } else {
-      store_part(mp + i, m, left[k]);
-      store_part(vp + i, v, left[k]);
-    }
+  } else if (whole) {
+    store_f8(mp + i, m);
+    store_f8(vp + i, v);
+  } else {
+    store_part(mp + i, m, left);
+    store_part(vp + i, v, left);
   }
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, kPerSm<FP8>) adamw_kernel(const __grid_constant__ Args a) {
   pdl_begin();
   const int step = a.step[0] + 1;
   Step st;
@@ -307,17 +303,17 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       if (a.first[mid] <= chunk) lo = mid; else hi = mid;
     }
     const Tensor& t = a.t[lo];
-    const int64_t i0 = (chunk - a.first[lo]) * kChunk + threadIdx.x * 8;
+    const int64_t i = (chunk - a.first[lo]) * kChunk + threadIdx.x * 8;
     using bf16 = __nv_bfloat16;
     if (t.master != nullptr) {
-      if (t.g_bf16) run_chunk<FP8, bf16, bf16, true>(a, t, i0, st);
-      else run_chunk<FP8, bf16, float, true>(a, t, i0, st);
+      if (t.g_bf16) run_chunk<FP8, bf16, bf16, true>(a, t, i, st);
+      else run_chunk<FP8, bf16, float, true>(a, t, i, st);
     } else if (t.p_bf16) {
-      if (t.g_bf16) run_chunk<FP8, bf16, bf16, false>(a, t, i0, st);
-      else run_chunk<FP8, bf16, float, false>(a, t, i0, st);
+      if (t.g_bf16) run_chunk<FP8, bf16, bf16, false>(a, t, i, st);
+      else run_chunk<FP8, bf16, float, false>(a, t, i, st);
     } else {
-      if (t.g_bf16) run_chunk<FP8, float, bf16, false>(a, t, i0, st);
-      else run_chunk<FP8, float, float, false>(a, t, i0, st);
+      if (t.g_bf16) run_chunk<FP8, float, bf16, false>(a, t, i, st);
+      else run_chunk<FP8, float, float, false>(a, t, i, st);
     }
   }
   // the block that comes last counts the step: all have read the old count
@@ -370,7 +366,7 @@ extern "C" int moe_adamw(const moe_adamw_config_t* c, const moe_adamw_tensor_t* 
   if (c == nullptr || n_tensors < 0 || (n_tensors > 0 && tensors == nullptr) || step == nullptr)
     return MOE_ERR_ARG;
   if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0) ||
-      !(c->eps > 0.0) || !std::isfinite(c->lr) || !std::isfinite(c->weight_decay))
+      !((float)c->eps >= FLT_MIN) || !std::isfinite(c->lr) || !std::isfinite(c->weight_decay))
     return MOE_ERR_ARG;
   if (host::misaligned(step, 4) || host::misaligned(lr, 4) || host::misaligned(grad_scale, 4))
     return MOE_ERR_ARG;
@@ -384,7 +380,6 @@ extern "C" int moe_adamw(const moe_adamw_config_t* c, const moe_adamw_tensor_t* 
   a.step = step; a.lr_dev = lr; a.grad_scale = grad_scale;
   // launches of up to MOE_ADAMW_MAX tensors of one state kind; the last one
   // counts the step (a list without elements still is a step)
-  const int64_t per_sm = 4;
   auto fill = [&](int from, bool fp8) {    // next tensors of a kind; where to go on
     a.n = 0;
     int64_t chunks = 0;
@@ -412,7 +407,7 @@ extern "C" int moe_adamw(const moe_adamw_config_t* c, const moe_adamw_tensor_t* 
       i = fill(i, fp8);
       a.last = !more(i, fp8) && (fp8 || !more(0, true));
       const int grid = (int)std::max<int64_t>(
-          1, std::min<int64_t>(a.first[a.n], (int64_t)host::sm_count() * per_sm));
+          1, std::min<int64_t>(a.first[a.n], (int64_t)host::sm_count() * (fp8 ? kPerSm<true> : kPerSm<false>) * kGrids));
       MOE_HTRY(host::launch("adamw", fp8 ? adamw_kernel<true> : adamw_kernel<false>, grid, kThreads,
                             0, s, 1, a));
       if (a.last) return MOE_OK;

@@ -230,18 +230,15 @@ int work_of(const moe_config_t* c, Work* w) {
 }
 
 template <int BN, int ST, int EPI, bool PAIR>
-int run_gemm(const char* name, const CUtensorMap& a, const CUtensorMap& a16, const CUtensorMap& b,
-             const CUtensorMap& bs, const CUtensorMap& o, const i8::Params& p, int64_t units,
-             cudaStream_t s) {
+int run_gemm(const char* name, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& bs,
+             const CUtensorMap& o, const i8::Params& p, int64_t units, cudaStream_t s) {
   using S = i8::Smem<BN, ST, PAIR>;
   auto k = i8::gemm_i8_kernel<BN, ST, EPI, PAIR>;
   MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes));
-  const int64_t items = units * p.nN;
-  if (items <= 0) return MOE_OK;
   int64_t resident = host::sm_count();
   if (PAIR) MOE_HTRY(host::resident_clusters(k, 2, tc::kThreads, S::kBytes, &resident));
-  const int ctas = (int)std::min<int64_t>(resident, items) * (PAIR ? 2 : 1);
-  return host::launch(name, k, ctas, tc::kThreads, S::kBytes, s, PAIR ? 2 : 1, a, a16, b, bs, o, p);
+  const int ctas = (int)std::min<int64_t>(resident, units * p.nN) * (PAIR ? 2 : 1);
+  return host::launch(name, k, ctas, tc::kThreads, S::kBytes, s, PAIR ? 2 : 1, a, b, bs, o, p);
 }
 
 // Row tiles per rasterisation group: as many row tiles of depth K bytes as
@@ -251,47 +248,56 @@ int group_rows(int64_t k_bytes, bool pair) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(64, (24ll << 20) / (rows * k_bytes)));
 }
 
+// Few rows per expert: the weights' way in bounds the product.
+bool few_rows(const moe_config_t* c, const Work& w) {
+  return (int64_t)c->T * c->K <= 32ll * w.v.local_experts;
+}
+
 template <int EPI>
 int product(const moe_config_t* c, const Work& w, const char* name, const int8_t* a, int64_t K,
             const int8_t* b, const int8_t* b_s, int64_t cols, void* out, i8::Params p,
             cudaStream_t s) {
   const bool pair = w.v.align == 256;
   const int64_t n_out = EPI == i8::I8_SWIGLU ? c->F : c->D;
-  // tiles that run at once: few row tiles (decoding) take narrow column
-  // tiles, so that every SM streams weights
-  const int64_t slots = (int64_t)c->T * c->K;
-  const int64_t mt = std::min<int64_t>(w.v.tiles_max,
-                                       std::min<int64_t>(w.v.local_experts, slots) +
-                                           slots / kRowTile + (c->n_shared ? host::ceil_div(c->T, 128) : 0));
-  const int sms = host::sm_count();
-  int bn = 256;
-  if (!pair) {
-    const int64_t tiles256 = mt * host::ceil_div(n_out, EPI == i8::I8_SWIGLU ? 128 : 256);
-    if (tiles256 < 2 * sms) bn = 128;
-    if (EPI == i8::I8_STORE && mt * host::ceil_div(n_out, 128) < 2 * sms) bn = 64;
+  const int64_t E = w.v.local_experts;
+  p.E = (int)E; p.F = c->F; p.nk = (int)(K / i8::kBK); p.cols = (int)cols;
+  CUtensorMap ma, mb, mbs, mo;
+  auto weights = [&](uint32_t box) {
+    MOE_HTRY(host::make_map_u8(&mb, b, E, cols, K, box));
+    return host::make_map_u8(&mbs, b_s != nullptr ? b_s : b, 1, cols, K, box);
+  };
+  if (few_rows(c, w)) {
+    auto k = i8::gemm_i8_thin_kernel<EPI>;
+    constexpr uint32_t box = EPI == i8::I8_SWIGLU ? 64 : 128;
+    p.nN = (int)(n_out / box);
+    p.group_m = 1;
+    MOE_HTRY(weights(box));
+    MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, K, 16));
+    i8::ThinParams tp{p, nullptr, nullptr};
+    if (EPI == i8::I8_SWIGLU) tp.h = static_cast<float*>(out);
+    else tp.o = static_cast<__nv_bfloat16*>(out);
+    MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 i8::ThinSmem::kBytes));
+    const int ctas = (int)std::min<int64_t>(host::sm_count(), w.v.tiles_max * p.nN);
+    return host::launch(name, k, ctas, tc::kThreads, i8::ThinSmem::kBytes, s, 1, mb, mbs, ma, tp);
   }
   // D and F are multiples of 128: a 256-wide plain tile may not divide D
-  if (EPI == i8::I8_STORE && n_out % bn) bn = 128;
-  const int tile_n = EPI == i8::I8_SWIGLU ? bn / 2 : bn;
-  p.E = w.v.local_experts; p.F = c->F; p.nk = (int)(K / i8::kBK); p.nN = (int)(n_out / tile_n);
-  p.group_m = group_rows(K, pair); p.cols = (int)cols;
-  CUtensorMap ma, ma16, mb, mbs, mo;
+  const int bn = EPI == i8::I8_STORE && n_out % 256 ? 128 : 256;
+  p.nN = (int)(n_out / (EPI == i8::I8_SWIGLU ? bn / 2 : bn));
+  p.group_m = group_rows(K, pair);
   MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, K, 128));
-  MOE_HTRY(host::make_map_u8(&ma16, a, 1, w.v.rows_max, K, 16));
-  const uint32_t box = (uint32_t)(EPI == i8::I8_SWIGLU || pair ? bn / 2 : bn);
-  MOE_HTRY(host::make_map_u8(&mb, b, w.v.local_experts, cols, K, box));
-  MOE_HTRY(host::make_map_u8(&mbs, b_s != nullptr ? b_s : b, 1, cols, K, box));
+  MOE_HTRY(weights((uint32_t)(EPI == i8::I8_SWIGLU || pair ? bn / 2 : bn)));
   MOE_HTRY(host::make_out_map(&mo, out, w.v.rows_max, n_out, EPI == i8::I8_SWIGLU));
   const int64_t units = w.v.tiles_max / (pair ? 2 : 1);
   if (pair) {
-    if (bn == 256) return run_gemm<256, 5, EPI, true>(name, ma, ma16, mb, mbs, mo, p, units, s);
-    return run_gemm<128, 6, EPI, true>(name, ma, ma16, mb, mbs, mo, p, units, s);
+    if (bn == 256) return run_gemm<256, 5, EPI, true>(name, ma, mb, mbs, mo, p, units, s);
+    if constexpr (EPI == i8::I8_STORE)
+      return run_gemm<128, 6, EPI, true>(name, ma, mb, mbs, mo, p, units, s);
   }
-  if (bn == 256) return run_gemm<256, 4, EPI, false>(name, ma, ma16, mb, mbs, mo, p, units, s);
   if constexpr (EPI == i8::I8_STORE) {
-    if (bn == 64) return run_gemm<64, 7, EPI, false>(name, ma, ma16, mb, mbs, mo, p, units, s);
+    if (bn == 128) return run_gemm<128, 5, EPI, false>(name, ma, mb, mbs, mo, p, units, s);
   }
-  return run_gemm<128, 5, EPI, false>(name, ma, ma16, mb, mbs, mo, p, units, s);
+  return run_gemm<256, 4, EPI, false>(name, ma, mb, mbs, mo, p, units, s);
 }
 
 template <typename TX>

@@ -13,9 +13,8 @@
 // accumulators in tensor memory, eight epilogue warps.  In bytes a stage is
 // the bf16 kernel's (128 bytes of k per row, now 128 elements), and every
 // MMA does twice the products on them, so the operands' way into the SM
-// bounds it sooner.  Tiles of few rows (decoding) load only the 16-row
-// pieces of A that hold tokens: the rest of the stage keeps whatever integers
-// it held, whose products land in accumulator rows that nothing stores.
+// bounds it sooner.  Experts of few rows (decoding) run in a second
+// kernel, at the end of this file.
 #pragma once
 #include "gemm_tc.cuh"
 
@@ -119,13 +118,11 @@ __device__ __forceinline__ Tile8 decode8(int t, const Params& p, int rank, int n
   return d;
 }
 
-// mapA: [rows_max][K] in 128-row boxes, mapA16: the same in 16-row boxes;
-// mapB / mapBs: [E][cols][K] (the shared expert's own); mapO: h [rows_max][F]
+// mapA: [rows_max][K]; mapB / mapBs: [E][cols][K] (the shared expert's own); mapO: h [rows_max][F]
 // fp32, or o [rows_max][D] bf16, for the epilogue's TMA stores.
 template <int BN, int STAGES, int EPI, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapA16,
-               const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapBs,
+gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapBs,
                const __grid_constant__ CUtensorMap mapO, const Params p) {
   using S = Smem<BN, STAGES, PAIR>;
   constexpr int NACC = S::NACC;
@@ -214,15 +211,12 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
         nxt = decode_at(t + n_units);
         const CUtensorMap* mb = d.e >= p.E ? &mapBs : &mapB;
         const int eb = d.e >= p.E ? 0 : d.e;
-        // pieces of A: one box of 128 rows, or up to four of 16 (single CTAs)
-        const int pieces = (PAIR || d.rows > 64) ? 0 : max(1, (d.rows + 15) / 16);
-        const uint32_t a_bytes = pieces == 0 ? S::kA : pieces * 16 * kBK;
         for (int kb = 0; kb < p.nk; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = base + stage * S::kStage;
           const uint32_t sb = sa + S::kA;
           const uint32_t fb = full_bar(stage);
-          if (!PAIR || leader) mbar_expect_tx(fb, PAIR ? 2 * (S::kA + S::kB) : a_bytes + S::kB);
+          if (!PAIR || leader) mbar_expect_tx(fb, (PAIR ? 2 : 1) * (S::kA + S::kB));
           issued_parity[stage] = (int)phase;
           const int k0 = kb * kBK;
           if constexpr (PAIR) {
@@ -237,12 +231,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
               tma_3d_pair(sbm, mb, lfb, k0, row, eb);
             }
           } else {
-            if (pieces == 0) {
-              tma_3d_hint(sa, &mapA, fb, k0, d.m0, 0, pol_a);
-            } else {
-              for (int i = 0; i < pieces; ++i)
-                tma_3d_hint(sa + i * 16 * kBK, &mapA16, fb, k0, d.m0 + 16 * i, 0, pol_a);
-            }
+            tma_3d_hint(sa, &mapA, fb, k0, d.m0, 0, pol_a);
             if (EPI == I8_SWIGLU) {
               tma_3d(sb, mb, fb, k0, d.n0, eb);
               tma_3d(sb + (BN / 2) * kBK, mb, fb, k0, p.F + d.n0, eb);
@@ -421,6 +410,284 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols)
                    : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Experts of few rows
+// ---------------------------------------------------------------------------
+// With a handful of tokens per expert a product is bound by reading its
+// weights once, so the operands change places: 128 weight rows are the MMA's
+// M side and the tokens its N side (16 to 64 of them, in steps of 16), and of
+// a stage's bytes all but the tokens' few are weights.  Nine stages of 16 KB
+// keep 144 KB of weights in flight per SM: under full load a copy takes
+// about 3 us from issue to arrival here, so DRAM's rate needs some 20 MB in
+// flight over the 148 SMs (the general kernel's narrow tiles held 8 MB and
+// read the Mixtral-shaped down projection at 2.7 TB/s).
+//
+// Accumulators are [channel][token]: a lane owns a channel, so a token's
+// outputs leave as coalesced 32-lane rows.  A gate/up tile holds 64 gate
+// rows (lanes 0-63) and the 64 up rows of the same channels (lanes 64-127);
+// the up warps pass their values through shared memory.  More than 64 tokens
+// in a 128-row tile run in turns over the same weights (the second turn
+// reads them from L2).
+constexpr int kThinTok = 64;
+constexpr int kThinStages = 9;
+struct ThinSmem {
+  static constexpr int kA = 128 * kBK;
+  static constexpr int kB = kThinTok * kBK;
+  static constexpr int kStage = kA + kB;
+  static constexpr int NACC = 4;
+  static constexpr int kBars = (2 * kThinStages + 2 * NACC + 1) * 8;
+  static constexpr int kEpiOff = (kThinStages * kStage + kBars + 16 + 127) / 128 * 128;
+  // the gate/up form's exchange buffer, [pair of warps][token][channel]
+  // fp32, replaces its ninth stage
+  static_assert(4 * 32 * 32 * 4 <= kStage, "exchange buffer");
+  static constexpr int kBytes = 1024 + kEpiOff;
+  static_assert(kBytes <= 232448 - 64, "shared memory per CTA");
+};
+template <int EPI> constexpr int thin_stages() { return EPI == I8_SWIGLU ? 8 : kThinStages; }
+
+// Both warps of a pair (64 threads, named barrier `bar`): whether v holds in both.
+__device__ __forceinline__ bool pair_and(int bar, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1 : 0), "r"(bar)
+      : "memory");
+  return r != 0;
+}
+
+struct ThinParams {
+  Params p;
+  float* h;                      // I8_SWIGLU out [rows_max, F]
+  __nv_bfloat16* o;              // I8_STORE out [rows_max, cols]
+};
+
+template <int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
+                    const __grid_constant__ CUtensorMap mapWs,
+                    const __grid_constant__ CUtensorMap mapT, const ThinParams tp) {
+  using S = ThinSmem;
+  const Params& p = tp.p;
+  constexpr int STAGES = thin_stages<EPI>(), NACC = S::NACC;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int abort_flag_s;
+  volatile int* abort_flag = &abort_flag_s;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + kThinStages * S::kStage;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (kThinStages + s); };
+  auto accf_bar = [&](int b) { return bars + 8u * (2 * kThinStages + b); };
+  auto acce_bar = [&](int b) { return bars + 8u * (2 * kThinStages + NACC + b); };
+  const uint32_t done_bar = bars + 8u * (2 * kThinStages + 2 * NACC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kThinStages * S::kStage + S::kBars);
+  float* swap = reinterpret_cast<float*>(gbase + (kThinStages - 1) * S::kStage);   // I8_SWIGLU
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr uint32_t kCols = NACC * kThinTok;
+  if (threadIdx.x == 0) {
+    abort_flag_s = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < NACC; ++b) {
+      mbar_init(accf_bar(b), 1);
+      mbar_init(acce_bar(b), kEpiWarps);
+    }
+    mbar_init(done_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 0) {
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_begin();
+
+  // a tile: 64 channels of F (gate and up rows), or 128 output channels
+  constexpr int kCh = EPI == I8_SWIGLU ? 64 : 128;
+  const int n_mt = p.stats[3];
+  const int total = n_mt * p.nN;
+  struct T {
+    int e, m0, n0, rows;
+  };
+  auto decode_at = [&](int t) {
+    if (t >= total) return T{0, 0, 0, 0};
+    // row tiles of one expert are neighbours and share its weights' columns
+    const int group = t / (p.group_m * p.nN), first = group * p.group_m;
+    const int gm = min(p.group_m, n_mt - first), local = t - group * p.group_m * p.nN;
+    const int mt = first + local % gm, nt = local / gm;
+    return T{p.tile_expert[mt], mt * BM, nt * kCh, p.tile_rows[mt]};
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued_parity[STAGES];
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
+      bool ok = true;
+      T nxt = decode_at(blockIdx.x);
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const T d = nxt;
+        nxt = decode_at(t + gridDim.x);
+        const CUtensorMap* mw = d.e >= p.E ? &mapWs : &mapW;
+        const int ew = d.e >= p.E ? 0 : d.e;
+        for (int r0 = 0; r0 < d.rows && ok; r0 += kThinTok) {
+          const int pieces = (min(kThinTok, d.rows - r0) + 15) / 16;
+          for (int kb = 0; kb < p.nk; ++kb) {
+            if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+            const uint32_t sw = base + stage * S::kStage, st = sw + S::kA;
+            const uint32_t fb = full_bar(stage);
+            mbar_expect_tx(fb, S::kA + pieces * 16 * kBK);
+            issued_parity[stage] = (int)phase;
+            const int k0 = kb * kBK;
+            if (EPI == I8_SWIGLU) {
+              tma_3d(sw, mw, fb, k0, d.n0, ew);
+              tma_3d(sw + 64 * kBK, mw, fb, k0, p.F + d.n0, ew);
+            } else {
+              tma_3d(sw, mw, fb, k0, d.n0, ew);
+            }
+            for (int i = 0; i < pieces; ++i)
+              tma_3d(st + i * 16 * kBK, &mapT, fb, k0, d.m0 + r0 + 16 * i, 0);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
+        }
+      }
+      for (int s = 0; s < STAGES; ++s)
+        if (issued_parity[s] >= 0) mbar_wait(full_bar(s), (uint32_t)issued_parity[s], abort_flag);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      T nxt = decode_at(blockIdx.x);
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const T d = nxt;
+        nxt = decode_at(t + gridDim.x);
+        for (int r0 = 0; r0 < d.rows && ok; r0 += kThinTok) {
+          const int n = (min(kThinTok, d.rows - r0) + 15) / 16 * 16;
+          const uint32_t idesc = idesc_i8(BM, n);
+          if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t dt = tmem + acc * kThinTok;
+          for (int kb = 0; kb < p.nk; ++kb) {
+            if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sw = base + stage * S::kStage, st = sw + S::kA;
+#pragma unroll
+            for (int ks = 0; ks < kBK / kUmmaK; ++ks)
+              umma_i8(dt, sw128_desc(sw + ks * kUmmaK, 16, 1024),
+                      sw128_desc(st + ks * kUmmaK, 16, 1024), idesc, (kb | ks) != 0 ? 1u : 0u);
+            umma_commit(empty_bar(stage));
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          umma_commit(accf_bar(acc));
+          if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
+        }
+      }
+      umma_commit(done_bar);
+      mbar_wait(done_bar, 0, abort_flag);
+    }
+  } else {
+    // Warp quarter q owns channels (lanes) 32 q ..; half hh the tokens
+    // 32 hh .. of the turn.
+    const int q = warp & 3, hh = (warp - 2) >> 2;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    T nxt = decode_at(blockIdx.x);
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const T d = nxt;
+      nxt = decode_at(t + gridDim.x);
+      const float* cs = d.e >= p.E ? p.col_scale_s : p.col_scale + (int64_t)d.e * p.cols;
+      // this lane's channel: of the outputs, or of F with its gate or up scale
+      const int ch = EPI == I8_SWIGLU ? d.n0 + (q & 1) * 32 + lane : d.n0 + q * 32 + lane;
+      const float ws = cs[EPI == I8_SWIGLU && q >= 2 ? p.F + ch : ch];
+      for (int r0 = 0; r0 < d.rows; r0 += kThinTok) {
+        const int row0 = d.m0 + r0 + hh * 32;
+        const int cnt = min(32, d.rows - r0 - hh * 32);   // tokens of this warp (may be <= 0)
+        float rs = 0.f;                                   // lane j: scale of token j
+        if (lane < cnt)
+          rs = EPI == I8_SWIGLU ? p.row_scale[row0 + lane] : scale_of(p.row_max[row0 + lane]);
+        ok = (lane == 0) ? mbar_wait(accf_bar(acc), acc_phase, abort_flag) : true;
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        // a gate warp and its up warp go on or give up together; past this
+        // both have also read the exchange buffer of the last turn
+        if (EPI == I8_SWIGLU) ok = pair_and(1 + (q & 1) + 2 * hh, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[32];
+        if (cnt > 0) {
+          tmem_ld32(tmem + acc * kThinTok + hh * 32 + ((uint32_t)(q * 32) << 16), r);
+          tmem_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acce_bar(acc));
+        if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
+        if (cnt <= 0) continue;
+        if constexpr (EPI == I8_SWIGLU) {
+          float* at = swap + ((q & 1) + 2 * hh) * 1024 + lane;
+          const int bar = 1 + (q & 1) + 2 * hh;           // the gate warp and the up warp
+          if (q >= 2) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < cnt)
+                at[j * 32] = __int2float_rn((int)r[j]) * (__shfl_sync(0xffffffffu, rs, j) * ws);
+            asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+          } else {
+            asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");   // the up values are there
+            float* h = tp.h + (int64_t)row0 * p.F + ch;
+            unsigned mine = 0;                            // lane j: largest |h| of token j
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (j < cnt) {
+                const float a = __int2float_rn((int)r[j]) * (__shfl_sync(0xffffffffu, rs, j) * ws);
+                const float v = a * fast_sigmoid(a) * at[j * 32];
+                h[(int64_t)j * p.F] = v;
+                const unsigned big = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
+                if (lane == j) mine = big;
+              }
+            }
+            if (lane < cnt) atomicMax(p.row_max + row0 + lane, mine);
+          }
+        } else {
+          __nv_bfloat16* o = tp.o + (int64_t)row0 * p.cols + ch;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < cnt)
+              o[(int64_t)j * p.cols] = __float2bfloat16_rn(
+                  __int2float_rn((int)r[j]) * (__shfl_sync(0xffffffffu, rs, j) * ws));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols)
+                 : "memory");
   }
 }
 

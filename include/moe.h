@@ -65,7 +65,7 @@ typedef enum {
 enum { MOE_FP32 = 0, MOE_BF16 = 1 };             /* cfg.dtype */
 enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 };       /* cfg.score_fn */
 enum { MOE_GMAX = 0, MOE_GTOP2SUM = 1 };         /* cfg.group_score */
-enum { MOE_GEMM_AUTO = 0, MOE_GEMM_SIMT = 1 };   /* cfg.gemm_impl */
+enum { MOE_GEMM_AUTO = 0, MOE_GEMM_SIMT = 1, MOE_GEMM_I8 = 2 };   /* cfg.gemm_impl */
 
 /* Device error word bits (moe_check_status). */
 #define MOE_DEVERR_EXPERT_ID  1u   /* an expert id outside [-1, E): slot treated as sentinel */
@@ -113,6 +113,9 @@ enum { MOE_GEMM_AUTO = 0, MOE_GEMM_SIMT = 1 };   /* cfg.gemm_impl */
  *   gemm_impl  MOE_GEMM_AUTO: tcgen05 tensor cores for bf16 when D and F
  *              are multiples of 128, CUDA-core SIMT otherwise (fp32 always);
  *              MOE_GEMM_SIMT: force the SIMT kernels (cross-checks).
+ *              MOE_GEMM_I8: as MOE_GEMM_AUTO, but rows are laid out for
+ *              moe_expert_ffn_i8, whose products run on CTA pairs (segments
+ *              aligned to 256 rows) from fewer rows per expert on.
  *   loss_tokens  0, or the global token count N >= T when the batch aux
  *              loss and the z-loss are scoped over all data-parallel ranks
  *              ([STA324 §8.5]: the balance statistic may be taken over the
@@ -664,7 +667,8 @@ int64_t moe_expert_ffn_i8_ws_bytes(const moe_config_t* cfg);
  *   o          [rows_max,D] act out: expert outputs, for moe_combine
  *   ws         workspace; calls that overlap need one each
  * bf16 token-choice layers with D and F multiples of 128, at most 65536
- * (MOE_ERR_ARG otherwise).  Expert shards (n_local_experts) hold their own
+ * (MOE_ERR_ARG otherwise); gemm_impl MOE_GEMM_I8 or MOE_GEMM_AUTO, the same
+ * as in the dispatch.  Expert shards (n_local_experts) hold their own
  * experts' weights.  A token with a NaN or an infinity gets NaN rows of o,
  * other tokens are not touched by it.
  */

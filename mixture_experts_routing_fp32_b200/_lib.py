@@ -16,7 +16,7 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_TIMEOUT = 0, -1, -2, 
 MOE_FP32, MOE_BF16 = 0, 1
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 MOE_GMAX, MOE_GTOP2SUM = 0, 1
-MOE_GEMM_AUTO, MOE_GEMM_SIMT = 0, 1
+MOE_GEMM_AUTO, MOE_GEMM_SIMT, MOE_GEMM_I8 = 0, 1, 2
 MOE_RMSNORM, MOE_LAYERNORM = 0, 1
 MOE_STATE_FP32, MOE_STATE_FP8 = 0, 1
 MOE_ADAMW_BLOCK = 256

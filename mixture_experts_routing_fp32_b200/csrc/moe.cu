@@ -131,7 +131,9 @@ int validate(const moe_config_t* c) {
   if (c->aux_alpha != 0.f && c->score_fn != MOE_SOFTMAX && c->seq_len == 0) return MOE_ERR_ARG;
   if (!(c->route_scale == c->route_scale) || c->min_capacity < 0) return MOE_ERR_ARG;
   if ((int64_t)c->T * c->K > (int64_t)INT32_MAX / 2) return MOE_ERR_ARG;
-  if (c->gemm_impl != MOE_GEMM_AUTO && c->gemm_impl != MOE_GEMM_SIMT) return MOE_ERR_ARG;
+  if (c->gemm_impl != MOE_GEMM_AUTO && c->gemm_impl != MOE_GEMM_SIMT &&
+      c->gemm_impl != MOE_GEMM_I8)
+    return MOE_ERR_ARG;
   // globally scoped batch losses: N >= T tokens; not for the sequence-wise
   // loss (its sequences live on one rank) or expert choice
   if (c->loss_tokens < 0 || (c->loss_tokens > 0 && c->loss_tokens < c->T)) return MOE_ERR_ARG;
@@ -144,7 +146,7 @@ int validate(const moe_config_t* c) {
   if (c->expert_base > 0 && c->n_local_experts == 0) return MOE_ERR_ARG;
   if (c->n_local_experts > 0 &&
       (c->expert_choice || c->n_shared || c->seq_len || c->dtype != MOE_BF16 ||
-       c->gemm_impl != MOE_GEMM_AUTO ||
+       c->gemm_impl == MOE_GEMM_SIMT ||
        (c->D % 128) || (c->F % 128)))
     return MOE_ERR_ARG;
   return MOE_OK;
@@ -174,7 +176,7 @@ int64_t capacity_of(const moe_config_t* c) {
 }
 
 bool use_tc(const moe_config_t* c) {
-  return c->dtype == MOE_BF16 && c->gemm_impl == MOE_GEMM_AUTO && (c->D % 128) == 0 &&
+  return c->dtype == MOE_BF16 && c->gemm_impl != MOE_GEMM_SIMT && (c->D % 128) == 0 &&
          (c->F % 128) == 0;
 }
 
@@ -251,7 +253,9 @@ bool pair_rows(const moe_config_t* c) {
   const int64_t kept = c->expert_choice ? (int64_t)c->E * ec_capacity(c)
                        : C < 0          ? slots
                                         : std::min<int64_t>(slots, (int64_t)c->E * C);
-  return kept / c->E >= 1536;
+  // 8-bit products do twice the work on the same operand bytes, so sharing
+  // them between two SMs pays sooner
+  return kept / c->E >= (c->gemm_impl == MOE_GEMM_I8 ? 512 : 1536);
 }
 
 int row_align(const moe_config_t* c) { return pair_rows(c) ? 256 : kRowTile; }

@@ -14,12 +14,14 @@ import ctypes
 import torch
 
 from . import api
-from ._lib import MoEError, MoeConfig, check, lib
+from ._lib import MOE_GEMM_AUTO, MOE_GEMM_I8, MoEError, MoeConfig, check, lib
 
 
 class MoEInt8Layer:
     def __init__(self, cfg, device="cuda"):
         c = self.cfg = MoeConfig.from_buffer_copy(cfg)
+        if c.gemm_impl == MOE_GEMM_AUTO:
+            c.gemm_impl = MOE_GEMM_I8
         self.ws_bytes = api.moe_expert_ffn_i8_ws_bytes(c)     # refuses what it cannot serve
         z = self.sizes = api.moe_get_sizes(c)
         dev = self.device = torch.device(device)

@@ -91,7 +91,7 @@ combine_bf16_kernel(const __nv_bfloat16* __restrict__ o, const int32_t* __restri
       g[k] = __shfl_sync(0xffffffffu, my_g, k);
     }
     const int64_t srow = n_shared ? shared0 + t : -1;
-    for (int d0 = lane * 8; d0 < D; d0 += 512) {
+    for (int d0 = lane * 8 + blockIdx.y * 512; d0 < D; d0 += 512 * gridDim.y) {
       const int d1 = d0 + 256;
       const bool has1 = d1 < D;
       uint4 r0[KT + 1], r1[KT + 1];
@@ -154,6 +154,8 @@ combine_bf16_kernel(const __nv_bfloat16* __restrict__ o, const int32_t* __restri
   }
 }
 
+// (blockIdx.y: a share of the columns' steps, so that few tokens still spread
+// over the SMs.)
 // bf16 combine for K <= 2: as combine_bf16_kernel, with four 256-column
 // chunks per step (more row loads in flight per warp for few rows per
 // token).  Same fixed k order and fp32 accumulation.
@@ -181,7 +183,7 @@ combine_bf16_wide_kernel(const __nv_bfloat16* __restrict__ o, const int32_t* __r
       g[k] = __shfl_sync(0xffffffffu, my_g, k);
     }
     rows[KT] = n_shared ? shared0 + t : -1;
-    for (int d0 = lane * 8; d0 < D; d0 += 256 * NC) {
+    for (int d0 = lane * 8 + blockIdx.y * 256 * NC; d0 < D; d0 += 256 * NC * gridDim.y) {
       uint4 r[NC][KT + 1];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {

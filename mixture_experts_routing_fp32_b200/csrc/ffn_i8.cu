@@ -12,7 +12,8 @@
 namespace moe {
 namespace {
 
-constexpr int kQThreads = 256;
+constexpr int kQThreads = 128;    // a row's threads: 16 columns each and turn
+constexpr int kHThreads = 256;
 constexpr int kMaxCols = 65536;
 
 // Power of two that keeps 127 v and the quotient's parts in range whatever
@@ -20,24 +21,20 @@ constexpr int kMaxCols = 65536;
 __device__ __forceinline__ float range_shift(float big) {
   return big < 7.9e-31f ? 1.8446744e19f : big > 1e36f ? 9.765625e-4f : 1.0f;   // 2^64, 2^-10
 }
-__device__ __forceinline__ int quantised(float v, float shift, float big) {
-  return __float2int_rn(127.0f * (v * shift) / big);
+__device__ __forceinline__ uint32_t pack4_i8(const int* q) {
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
 }
-__device__ __forceinline__ uint2 pack8_i8(const int* q) {
-  uint2 u;
-  u.x = (q[0] & 255) | ((q[1] & 255) << 8) | ((q[2] & 255) << 16) | ((uint32_t)q[3] << 24);
-  u.y = (q[4] & 255) | ((q[5] & 255) << 8) | ((q[6] & 255) << 16) | ((uint32_t)q[7] << 24);
-  return u;
+__device__ __forceinline__ uint4 pack16_i8(const int* q) {
+  return make_uint4(pack4_i8(q), pack4_i8(q + 4), pack4_i8(q + 8), pack4_i8(q + 12));
 }
-// Largest magnitude's bits over a block (NaN orders above infinity).
+// Largest magnitude's bits over the block (NaN orders above infinity).
 __device__ __forceinline__ unsigned block_max(unsigned v, unsigned* red) {
   v = __reduce_max_sync(0xffffffffu, v);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();            // the previous row's readers are done
   if (lane == 0) red[warp] = v;
   __syncthreads();
-  v = lane < (kQThreads >> 5) ? red[lane] : 0u;
-  return __reduce_max_sync(0xffffffffu, v);
+  return max(max(red[0], red[1]), max(red[2], red[3]));
 }
 __device__ __forceinline__ unsigned max_bits(const float* f, unsigned m) {
 #pragma unroll
@@ -45,31 +42,33 @@ __device__ __forceinline__ unsigned max_bits(const float* f, unsigned m) {
   return m;
 }
 
-// One row per block and turn, NV pieces of 8 columns per thread held in
-// registers between the maximum and the rounding; NV = 0: rows longer than
-// that are read twice (the second time from L2).  out(col, packed) stores 8
-// values; the scale is returned.
+// One row per block and turn: NV pieces of 16 columns per thread (the last
+// one 8 where the row ends) stay in registers between the maximum and the
+// rounding; NV = 0: rows longer than that are read twice (the second time
+// from L2).  out(col, u) stores 16 values, out(col, lower half, true) 8; the
+// scale is returned.
 template <typename TX, int NV, typename Out>
 __device__ __forceinline__ float quantise_row(const TX* x, int cols, unsigned* red, Out out) {
-  const int nv = cols / 8;
   unsigned m = 0;
-  Raw8<TX> keep[NV > 0 ? NV : 1];
+  constexpr int kStep = kQThreads * 16;
+  Raw8<TX> keep[NV > 0 ? 2 * NV : 1];
+  const int c0 = threadIdx.x * 16;
   if constexpr (NV > 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = threadIdx.x + i * kQThreads;
-      if (c < nv) keep[i].load(x + 8 * (int64_t)c);
+    for (int i = 0; i < 2 * NV; ++i) {
+      const int c = c0 + (i >> 1) * kStep + (i & 1) * 8;
+      if (c < cols) keep[i].load(x + c);
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < 2 * NV; ++i) {
       float f[8];
       keep[i].widen(f);
-      if (threadIdx.x + i * kQThreads < nv) m = max_bits(f, m);
+      if (c0 + (i >> 1) * kStep + (i & 1) * 8 < cols) m = max_bits(f, m);
     }
   } else {
-    for (int c = threadIdx.x; c < nv; c += kQThreads) {
+    for (int c = threadIdx.x * 8; c < cols; c += kQThreads * 8) {
       float f[8];
-      load8(x + 8 * (int64_t)c, f);
+      load8(x + c, f);
       m = max_bits(f, m);
     }
   }
@@ -77,25 +76,33 @@ __device__ __forceinline__ float quantise_row(const TX* x, int cols, unsigned* r
   const bool finite = m < 0x7f800000u;
   const float big = __uint_as_float(m);
   const float shift = range_shift(big), den = big > 0.f ? big * shift : 1.0f;
-  auto put = [&](const float* f, int c) {
-    int q[8];
+  auto round8 = [&](const float* f, int* q) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = finite ? quantised(f[i], shift, den) : 0;
-    out(8 * c, pack8_i8(q));
+    for (int i = 0; i < 8; ++i) q[i] = finite ? __float2int_rn(127.0f * (f[i] * shift) / den) : 0;
   };
   if constexpr (NV > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = threadIdx.x + i * kQThreads;
-      float f[8];
-      keep[i].widen(f);
-      if (c < nv) put(f, c);
+      const int c = c0 + i * kStep;
+      if (c < cols) {
+        float f[8];
+        int q[16];
+        keep[2 * i].widen(f);
+        round8(f, q);
+        keep[2 * i + 1].widen(f);
+        round8(f, q + 8);        // (unused values behind the row's end)
+        out(c, pack16_i8(q), c + 16 <= cols);
+      }
     }
   } else {
-    for (int c = threadIdx.x; c < nv; c += kQThreads) {
+    for (int c = threadIdx.x * 16; c < cols; c += kStep) {
       float f[8];
-      load8(x + 8 * (int64_t)c, f);
-      put(f, c);
+      int q[16];
+      load8(x + c, f);
+      round8(f, q);
+      if (c + 16 <= cols) load8(x + c + 8, f);
+      round8(f, q + 8);
+      out(c, pack16_i8(q), c + 16 <= cols);
     }
   }
   return i8::scale_of(m);
@@ -104,12 +111,18 @@ __device__ __forceinline__ float quantise_row(const TX* x, int cols, unsigned* r
 template <typename TX, int NV>
 __global__ void __launch_bounds__(kQThreads)
 quant_rows_kernel(const TX* x, int64_t rows, int cols, int64_t ld, int8_t* q, float* scale) {
-  __shared__ unsigned red[32];
+  __shared__ unsigned red[kQThreads / 32];
+  const bool wide = (cols & 15) == 0 && (reinterpret_cast<uintptr_t>(q) & 15) == 0;
   pdl_begin();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     int8_t* dst = q + r * cols;
-    const float s = quantise_row<TX, NV>(x + r * ld, cols, red, [&](int c, uint2 u) {
-      *reinterpret_cast<uint2*>(dst + c) = u;
+    const float s = quantise_row<TX, NV>(x + r * ld, cols, red, [&](int c, uint4 u, bool whole) {
+      if (wide) {
+        *reinterpret_cast<uint4*>(dst + c) = u;
+      } else {
+        *reinterpret_cast<uint2*>(dst + c) = make_uint2(u.x, u.y);
+        if (whole) *reinterpret_cast<uint2*>(dst + c + 8) = make_uint2(u.z, u.w);
+      }
     });
     if (threadIdx.x == 0) scale[r] = s;
   }
@@ -126,10 +139,11 @@ quant_dispatch_kernel(const __nv_bfloat16* x, int T, int D, int K, int E, int n_
                       const int32_t* offsets, const int32_t* slot_row, const int32_t* row_slot,
                       const int32_t* stats, int token_blocks, int8_t* xq, float* scale,
                       unsigned* row_max, int32_t* tile_rows) {
-  __shared__ unsigned red[32];
+  __shared__ unsigned red[kQThreads / 32];
+  const int lane = threadIdx.x & 31;
   pdl_begin();
   if ((int)blockIdx.x >= token_blocks) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const int n_tiles = stats[3], shared0 = offsets[E] / kRowTile;
     const int step = (gridDim.x - token_blocks) * (kQThreads >> 5);
     for (int t = (blockIdx.x - token_blocks) * (kQThreads >> 5) + warp; t < n_tiles; t += step) {
@@ -145,24 +159,32 @@ quant_dispatch_kernel(const __nv_bfloat16* x, int T, int D, int K, int E, int n_
     }
     return;
   }
-  const int shared_row = n_shared ? offsets[E] : -1;
-  for (int t = blockIdx.x; t < T; t += token_blocks) {
-    const int32_t* rows = slot_row + (int64_t)t * K;
+  // the rows that hold the token, compacted by the first warp (K is at most
+  // 16); two lists take turns, so that a warp still reading one is behind a
+  // barrier of the row in between
+  __shared__ int held_s[2][32];
+  __shared__ int n_held_s[2];
+  const int shared_row = n_shared ? offsets[E] : 0;
+  int turn = 0;
+  for (int t = blockIdx.x; t < T; t += token_blocks, turn ^= 1) {
+    int row = -1;
+    if (threadIdx.x < 32) {
+      if (lane < K) row = slot_row[(int64_t)t * K + lane];
+      else if (lane == K && n_shared) row = shared_row + t;
+      const unsigned some = __ballot_sync(0xffffffffu, row >= 0);
+      if (row >= 0) held_s[turn][__popc(some & ((1u << lane) - 1u))] = row;
+      if (lane == 0) n_held_s[turn] = __popc(some);
+    }
+    // (the barriers of the row's maximum publish the list)
     const float s = quantise_row<__nv_bfloat16, NV>(
-        x + (int64_t)t * D, D, red, [&](int c, uint2 u) {
-          for (int k = 0; k < K; ++k) {
-            const int r = rows[k];
-            if (r >= 0) *reinterpret_cast<uint2*>(xq + (int64_t)r * D + c) = u;
-          }
-          if (shared_row >= 0)
-            *reinterpret_cast<uint2*>(xq + (int64_t)(shared_row + t) * D + c) = u;
+        x + (int64_t)t * D, D, red, [&](int c, uint4 u, bool) {
+          const int n = n_held_s[turn];
+          for (int k = 0; k < n; ++k)
+            *reinterpret_cast<uint4*>(xq + (int64_t)held_s[turn][k] * D + c) = u;
         });
-    for (int k = threadIdx.x; k <= K; k += kQThreads) {
-      const int r = k < K ? rows[k] : shared_row >= 0 ? shared_row + t : -1;
-      if (r >= 0) {
-        scale[r] = s;
-        row_max[r] = 0u;
-      }
+    if (row >= 0) {
+      scale[row] = s;
+      row_max[row] = 0u;
     }
   }
 }
@@ -170,15 +192,15 @@ quant_dispatch_kernel(const __nv_bfloat16* x, int T, int D, int K, int E, int n_
 // h (fp32, each row's largest magnitude already known from the product's
 // epilogue) to 8 bits: 16 columns a thread, 512 a warp and turn.  h is fp32,
 // where ties mean nothing, so the quotient is a product with 127 / max.
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kHThreads)
 quant_h_kernel(const float* h, int F, const int32_t* stats, const int32_t* tile_rows,
                const unsigned* row_max, int8_t* hq) {
   pdl_begin();
   const int lane = threadIdx.x & 31;
   const int per = (F + 511) / 512;
   const int64_t total = (int64_t)stats[2] * per;
-  const int64_t step = (int64_t)gridDim.x * (kQThreads >> 5);
-  for (int64_t u = (int64_t)blockIdx.x * (kQThreads >> 5) + (threadIdx.x >> 5); u < total;
+  const int64_t step = (int64_t)gridDim.x * (kHThreads >> 5);
+  for (int64_t u = (int64_t)blockIdx.x * (kHThreads >> 5) + (threadIdx.x >> 5); u < total;
        u += step) {
     const int64_t r = u / per;
     const int c = (int)(u - r * per) * 512 + lane * 16;
@@ -193,8 +215,7 @@ quant_h_kernel(const float* h, int F, const int32_t* stats, const int32_t* tile_
     int q[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) q[i] = inv > 0.f ? __float2int_rn(f[i] * shift * inv) : 0;
-    const uint2 a = pack8_i8(q), b = pack8_i8(q + 8);
-    *reinterpret_cast<uint4*>(hq + r * F + c) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(hq + r * F + c) = pack16_i8(q);
   }
 }
 
@@ -303,8 +324,8 @@ int product(const moe_config_t* c, const Work& w, const char* name, const int8_t
 template <typename TX>
 int quant_rows(const TX* x, int64_t rows, int64_t cols, int64_t ld, int8_t* q, float* scale,
                cudaStream_t s) {
-  const int grid = (int)std::min<int64_t>(rows, (int64_t)host::sm_count() * 8);
-  const int64_t nv = host::ceil_div(cols / 8, kQThreads);
+  const int grid = (int)std::min<int64_t>(rows, (int64_t)host::sm_count() * 16);
+  const int64_t nv = host::ceil_div(cols, kQThreads * 16);
   auto go = [&](auto k) {
     return host::launch("quant_i8", k, grid, kQThreads, 0, s, 1, x, rows, (int)cols, ld, q, scale);
   };
@@ -375,7 +396,7 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
   int32_t* tile_rows = reinterpret_cast<int32_t*>(base + w.tile_rows);
   const int sms = host::sm_count();
   {
-    const int tokens = (int)std::min<int64_t>(c->T, (int64_t)sms * 8);
+    const int tokens = (int)std::min<int64_t>(c->T, (int64_t)sms * 16);
     const int tiles = (int)std::min<int64_t>(host::ceil_div(w.v.tiles_max, kQThreads / 32), 64);
     auto go = [&](auto k) {
       return host::launch("quant_dispatch", k, tokens + tiles, kQThreads, 0, s, 1,
@@ -383,7 +404,7 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
                           w.v.local_experts, c->n_shared, offsets, slot_row, row_slot, stats,
                           tokens, xq, xs, row_max, tile_rows);
     };
-    const int64_t nv = host::ceil_div(c->D / 8, kQThreads);
+    const int64_t nv = host::ceil_div(c->D, kQThreads * 16);
     if (nv <= 1) MOE_HTRY(go(quant_dispatch_kernel<1>));
     else if (nv <= 2) MOE_HTRY(go(quant_dispatch_kernel<2>));
     else if (nv <= 4) MOE_HTRY(go(quant_dispatch_kernel<4>));
@@ -398,7 +419,7 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
   MOE_HTRY(host::launch("quant_h", quant_h_kernel,
                         (int)std::min<int64_t>(host::ceil_div(w.v.rows_max * host::ceil_div(c->F, 512), 8),
                                                (int64_t)sms * 8),
-                        kQThreads, 0, s, 1, h, c->F, stats, tile_rows, row_max, hq));
+                        kHThreads, 0, s, 1, h, c->F, stats, tile_rows, row_max, hq));
   p.col_scale = w_down_scale; p.col_scale_s = w_down_s_scale;
   return product<i8::I8_STORE>(c, w, "i8_down", hq, c->F, w_down, w_down_s, c->D, o, p, s);
 }

@@ -87,7 +87,7 @@ __device__ __forceinline__ float scale_of(unsigned bits) {
 template <int BN, int STAGES, bool PAIR>
 struct Smem {
   static constexpr int BNC = PAIR ? BN / 2 : BN;      // columns of B this CTA holds
-  static constexpr int NACC = BN <= 128 ? 4 : BN <= 256 ? 2 : 1;
+  static constexpr int NACC = BN <= 128 ? 4 : 2;
   static constexpr int kA = BM * kBK;
   static constexpr int kB = BNC * kBK;
   static constexpr int kStage = kA + kB;
@@ -126,10 +126,6 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
                const __grid_constant__ CUtensorMap mapO, const Params p) {
   using S = Smem<BN, STAGES, PAIR>;
   constexpr int NACC = S::NACC;
-  constexpr int NBM = BN > 256 ? BN / 256 : 1;       // MMAs per k step (N at most 256 each)
-  constexpr int NMM = BN / NBM;
-  constexpr int BLK = PAIR ? NMM / 2 : NMM;          // B rows per CTA and MMA
-  static_assert(BN <= 256 || PAIR, "512-wide tiles only on CTA pairs");
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   volatile int* abort_flag = &abort_flag_s;
@@ -149,8 +145,8 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   const bool leader = rank == 0;
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   const int n_units = PAIR ? gridDim.x >> 1 : gridDim.x;
-  constexpr uint32_t kCols = (NACC * BN <= 256) ? 256u : 512u;
-  static_assert(NACC * BN <= 512, "tensor-memory columns");
+  constexpr uint32_t kCols = 512;
+  static_assert(NACC * BN == kCols, "tensor-memory columns");
 
   if (threadIdx.x == 0) {
     abort_flag_s = 0;
@@ -222,14 +218,9 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
           if constexpr (PAIR) {
             const uint32_t lfb = mapa(fb, 0);
             tma_3d_pair_hint(sa, &mapA, lfb, k0, d.m0, 0, pol_a);
-#pragma unroll
-            for (int m = 0; m < NBM; ++m) {
-              const uint32_t sbm = sb + m * BLK * kBK;
-              // SwiGLU: this CTA holds the gate (rank 0) or the up (rank 1) rows
-              const int row = EPI == I8_SWIGLU ? (rank ? p.F : 0) + d.n0 + m * BLK
-                                               : d.n0 + m * NMM + rank * BLK;
-              tma_3d_pair(sbm, mb, lfb, k0, row, eb);
-            }
+            // SwiGLU: this CTA holds the gate (rank 0) or the up (rank 1) rows
+            tma_3d_pair(sb, mb, lfb, k0,
+                        EPI == I8_SWIGLU ? (rank ? p.F : 0) + d.n0 : d.n0 + rank * (BN / 2), eb);
           } else {
             tma_3d_hint(sa, &mapA, fb, k0, d.m0, 0, pol_a);
             if (EPI == I8_SWIGLU) {
@@ -250,7 +241,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   } else if (warp == 1) {
     // ---------------- MMA issuer (the pair leader only) ----------------
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc = idesc_i8(PAIR ? 2 * BM : BM, NMM);
+      constexpr uint32_t idesc = idesc_i8(PAIR ? 2 * BM : BM, BN);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -268,12 +259,9 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
 #pragma unroll
           for (int ks = 0; ks < kBK / kUmmaK; ++ks) {
             const uint64_t ad = sw128_desc(sa + ks * kUmmaK, 16, 1024);
-#pragma unroll
-            for (int m = 0; m < NBM; ++m) {
-              const uint64_t bd = sw128_desc(sb + m * BLK * kBK + ks * kUmmaK, 16, 1024);
-              if constexpr (PAIR) umma_i8_pair(dt + m * NMM, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
-              else umma_i8(dt + m * NMM, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
-            }
+            const uint64_t bd = sw128_desc(sb + ks * kUmmaK, 16, 1024);
+            if constexpr (PAIR) umma_i8_pair(dt, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
+            else umma_i8(dt, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
           }
           if constexpr (PAIR) umma_commit_pair_both(empty_bar(stage));
           else umma_commit(empty_bar(stage));
@@ -313,18 +301,17 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
       const uint32_t trow = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
       if (any) {
         if constexpr (EPI == I8_SWIGLU) {
-          // MMA m of the tile holds gate columns [0, NMM/2) and up columns
-          // behind them, for F columns n0 + m NMM/2 + ...
-          constexpr int HB = NMM / 2;                   // gate columns per MMA
-          constexpr int HJ = HB / 2;                    // this warp's share of them
+          // gate columns [0, HB) and up columns behind them, for F columns
+          // n0 ..
+          constexpr int HB = BN / 2, HJ = HB / 2;       // HJ: this warp's share
           unsigned big = 0;
 #pragma unroll 1
-          for (int c = 0; c < NBM * HJ; c += 32) {
-            const int m = c / HJ, j = hh * HJ + c % HJ;   // column inside the MMA's gate half
+          for (int c = 0; c < HJ; c += 32) {
+            const int j = hh * HJ + c;
             uint32_t ra[32], rb[32];
-            tmem_ld32(trow + m * NMM + j, ra);
-            tmem_ld32(trow + m * NMM + HB + j, rb);
-            const int f0 = d.n0 + m * HB + j;
+            tmem_ld32(trow + j, ra);
+            tmem_ld32(trow + HB + j, rb);
+            const int f0 = d.n0 + j;
             const float4* ca = reinterpret_cast<const float4*>(cs + f0);
             const float4* cb = reinterpret_cast<const float4*>(cs + p.F + f0);
             tmem_wait();
@@ -448,6 +435,11 @@ struct ThinSmem {
 };
 template <int EPI> constexpr int thin_stages() { return EPI == I8_SWIGLU ? 8 : kThinStages; }
 
+// Bytes to come on `bar`, without an arrival.
+__device__ __forceinline__ void mbar_expect_only(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
 // Both warps of a pair (64 threads, named barrier `bar`): whether v holds in both.
 __device__ __forceinline__ bool pair_and(int bar, bool v) {
   uint32_t r;
@@ -517,11 +509,10 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_begin();
 
   // a tile: 64 channels of F (gate and up rows), or 128 output channels
   constexpr int kCh = EPI == I8_SWIGLU ? 64 : 128;
-  const int n_mt = p.stats[3];
+  const int n_mt = __ldcg(p.stats + 3);
   const int total = n_mt * p.nN;
   struct T {
     int e, m0, n0, rows;
@@ -532,8 +523,34 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
     const int group = t / (p.group_m * p.nN), first = group * p.group_m;
     const int gm = min(p.group_m, n_mt - first), local = t - group * p.group_m * p.nN;
     const int mt = first + local % gm, nt = local / gm;
-    return T{p.tile_expert[mt], mt * BM, nt * kCh, p.tile_rows[mt]};
+    // (a tile in use holds a row; one without would leave requested weights
+    // unused)
+    return T{__ldcg(p.tile_expert + mt), mt * BM, nt * kCh, max(1, __ldcg(p.tile_rows + mt))};
   };
+  auto load_weights = [&](const CUtensorMap* mw, uint32_t sw, uint32_t fb, int k0, int n0, int ew) {
+    tma_3d(sw, mw, fb, k0, n0, ew);
+    if (EPI == I8_SWIGLU) tma_3d(sw + 64 * kBK, mw, fb, k0, p.F + n0, ew);
+  };
+  // The first stages' weights are requested before the wait for the previous
+  // kernel of the stream: they and the dispatch's tables are older than it
+  // (each kernel here lets its successor start only once its own predecessor
+  // is complete, and between the dispatch and either product runs another
+  // kernel), so their way overlaps that kernel.  The stage's barrier is told
+  // of the bytes without an arrival; that follows with the tokens' bytes.
+  int early = 0;
+  if (warp == 0 && lane == 0 && (int)blockIdx.x < total) {
+    const int t = blockIdx.x;
+    const int group = t / (p.group_m * p.nN), first = group * p.group_m;
+    const int gm = min(p.group_m, n_mt - first), local = t - group * p.group_m * p.nN;
+    const int e = __ldcg(p.tile_expert + first + local % gm), n0 = local / gm * kCh;
+    early = min(STAGES, p.nk);
+    for (int s = 0; s < early; ++s) {
+      mbar_expect_only(full_bar(s), S::kA);
+      load_weights(e >= p.E ? &mapWs : &mapW, base + s * S::kStage, full_bar(s), s * kBK, n0,
+                   e >= p.E ? 0 : e);
+    }
+  }
+  pdl_begin();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -541,7 +558,7 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
       uint32_t phase = 0;
       int issued_parity[STAGES];
 #pragma unroll
-      for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
+      for (int s = 0; s < STAGES; ++s) issued_parity[s] = s < early ? 0 : -1;
       bool ok = true;
       T nxt = decode_at(blockIdx.x);
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -555,15 +572,15 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
             if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
             const uint32_t sw = base + stage * S::kStage, st = sw + S::kA;
             const uint32_t fb = full_bar(stage);
-            mbar_expect_tx(fb, S::kA + pieces * 16 * kBK);
-            issued_parity[stage] = (int)phase;
             const int k0 = kb * kBK;
-            if (EPI == I8_SWIGLU) {
-              tma_3d(sw, mw, fb, k0, d.n0, ew);
-              tma_3d(sw + 64 * kBK, mw, fb, k0, p.F + d.n0, ew);
+            if (early > 0) {              // weights on their way already
+              --early;
+              mbar_expect_tx(fb, pieces * 16 * kBK);
             } else {
-              tma_3d(sw, mw, fb, k0, d.n0, ew);
+              mbar_expect_tx(fb, S::kA + pieces * 16 * kBK);
+              load_weights(mw, sw, fb, k0, d.n0, ew);
             }
+            issued_parity[stage] = (int)phase;
             for (int i = 0; i < pieces; ++i)
               tma_3d(st + i * 16 * kBK, &mapT, fb, k0, d.m0 + r0 + 16 * i, 0);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }

@@ -20,8 +20,30 @@ def _p(t):
 
 
 def _s(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The stream's handle (by default the current stream's, asked for
+    directly: building torch's Stream object takes 3 us)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
+def _args(what, stream, *specs):
+    """Pointers of (name, tensor, dtype, elements) and the stream's handle.
+    Refuses tensors that are not what a kernel would read: other types or
+    sizes, strided ones, ones that are not on the current device."""
+    dev = torch._C._cuda_getDevice()
+    out = []
+    for name, t, dt, n in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype != dt or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+            raise MoEError(
+                "%s: %s is not a contiguous tensor of %d x %s on the current device (cuda:%d): "
+                "%s x %s on %s" % (what, name, n, dt, dev, tuple(t.shape), t.dtype, t.device))
+        out.append(t.data_ptr())
+    out.append(torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    return out
 
 
 def make_config(T, D, E, K, F, *, n_shared=0, dtype="bf16", score_fn=0,
@@ -193,12 +215,20 @@ def make_norm_config(T, D, *, norm="rms", dtype="bf16", resid=None, eps=1e-5, al
                       eps=eps, alpha=alpha)
 
 
+_TYPES = {C.MOE_FP32: torch.float32, C.MOE_BF16: torch.bfloat16}
+
+
 def moe_block_norm(cfg, r, y, w_post, b_post, gate, w_pre, b_pre, r_out, x, stats,
                    stream=None):
     """r_out = r + alpha gate N(y); x = N(r_out) (y None: x = N(r) alone)."""
-    check(lib().moe_block_norm(ctypes.byref(cfg), _p(r), _p(y), _p(w_post), _p(b_post),
-                               _p(gate), _p(w_pre), _p(b_pre), _p(r_out), _p(x), _p(stats),
-                               _s(stream)), "moe_block_norm")
+    T, D, L, f32 = cfg.T, cfg.D, cfg.gate_len, torch.float32
+    n, act, res = T * D, _TYPES[cfg.dtype], _TYPES[cfg.resid]
+    check(lib().moe_block_norm(ctypes.byref(cfg), *_args(
+        "moe_block_norm", stream, ("r", r, res, n), ("y", y, act, n),
+        ("w_post", w_post, f32, D), ("b_post", b_post, f32, D),
+        ("gate", gate, f32, -(-T // L) * D if L > 0 else 0), ("w_pre", w_pre, f32, D),
+        ("b_pre", b_pre, f32, D), ("r_out", r_out, res, n), ("x", x, act, n),
+        ("stats", stats, f32, 4 * T))), "moe_block_norm")
 
 
 def moe_block_norm_ws_bytes(cfg) -> int:
@@ -211,10 +241,19 @@ def moe_block_norm_ws_bytes(cfg) -> int:
 
 def moe_block_norm_backward(cfg, r_out, y, w_post, b_post, gate, w_pre, stats, dx, dr_out, dy,
                             dr, dw_post, db_post, dgate, dw_pre, db_pre, ws, stream=None):
-    check(lib().moe_block_norm_backward(
-        ctypes.byref(cfg), _p(r_out), _p(y), _p(w_post), _p(b_post), _p(gate), _p(w_pre),
-        _p(stats), _p(dx), _p(dr_out), _p(dy), _p(dr), _p(dw_post), _p(db_post), _p(dgate),
-        _p(dw_pre), _p(db_pre), _p(ws), _s(stream)), "moe_block_norm_backward")
+    T, D, L, f32 = cfg.T, cfg.D, cfg.gate_len, torch.float32
+    n, act, res = T * D, _TYPES[cfg.dtype], _TYPES[cfg.resid]
+    g = -(-T // L) * D if L > 0 else 0
+    if ws is not None and ws.numel() < moe_block_norm_ws_bytes(cfg):
+        raise MoEError("moe_block_norm_backward: the workspace is too small")
+    check(lib().moe_block_norm_backward(ctypes.byref(cfg), *_args(
+        "moe_block_norm_backward", stream, ("r_out", r_out, res, n), ("y", y, act, n),
+        ("w_post", w_post, f32, D), ("b_post", b_post, f32, D), ("gate", gate, f32, g),
+        ("w_pre", w_pre, f32, D), ("stats", stats, f32, 4 * T), ("dx", dx, act, n),
+        ("dr_out", dr_out, res, n), ("dy", dy, act, n), ("dr", dr, res, n),
+        ("dw_post", dw_post, f32, D), ("db_post", db_post, f32, D), ("dgate", dgate, f32, g),
+        ("dw_pre", dw_pre, f32, D), ("db_pre", db_pre, f32, D),
+        ("ws", ws, torch.uint8, 0 if ws is None else ws.numel()))), "moe_block_norm_backward")
 
 
 def make_adamw_config(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
@@ -271,8 +310,13 @@ def adamw_table(entries) -> AdamwTable:
 def moe_adamw(cfg, table, step, lr=None, grad_scale=None, stream=None):
     """One AdamW step over an adamw_table; step: int32 [2] device tensor (the
     count of steps taken, and a word of the kernel's own that starts at 0)."""
-    check(lib().moe_adamw(ctypes.byref(cfg), table.array, table.count, _p(step), _p(lr),
-                          _p(grad_scale), _s(stream)), "moe_adamw")
+    dev = torch._C._cuda_getDevice()
+    if table.device is not None and table.device.index != dev:
+        raise MoEError("moe_adamw: the tensors are on %s, the current device is cuda:%d"
+                       % (table.device, dev))
+    *p, s = _args("moe_adamw", stream, ("step", step, torch.int32, 2),
+                  ("lr", lr, torch.float32, 1), ("grad_scale", grad_scale, torch.float32, 1))
+    check(lib().moe_adamw(ctypes.byref(cfg), table.array, table.count, *p, s), "moe_adamw")
 
 
 def moe_quant_i8(x, q, scale, stream=None):
@@ -292,8 +336,12 @@ def moe_quant_i8(x, q, scale, stream=None):
             or scale.dtype != torch.float32 or scale.shape != x.shape[:-1]
             or not scale.is_contiguous()):
         raise MoEError("moe_quant_i8: q is int8 like x, scale fp32 with a value per row")
-    check(lib().moe_quant_i8(_p(x), _dtype(x.dtype), rows, cols, ld, _p(q), _p(scale),
-                             _s(stream)), "moe_quant_i8")
+    pq, ps, s = _args("moe_quant_i8", stream, ("q", q, torch.int8, rows * cols),
+                      ("scale", scale, torch.float32, rows))
+    if x.get_device() != q.get_device():
+        raise MoEError("moe_quant_i8: x is on %s, q on %s" % (x.device, q.device))
+    check(lib().moe_quant_i8(x.data_ptr(), _dtype(x.dtype), rows, cols, ld, pq, ps, s),
+          "moe_quant_i8")
 
 
 def moe_expert_ffn_i8_ws_bytes(cfg) -> int:
@@ -307,10 +355,22 @@ def moe_expert_ffn_i8_ws_bytes(cfg) -> int:
 def moe_expert_ffn_i8(cfg, x, offsets, slot_row, row_slot, tile_expert, stats, w13, w13_scale,
                       w_down, w_down_scale, w13_s, w13_s_scale, w_down_s, w_down_s_scale, o, ws,
                       stream=None):
-    check(lib().moe_expert_ffn_i8(
-        ctypes.byref(cfg), _p(x), _p(offsets), _p(slot_row), _p(row_slot), _p(tile_expert),
-        _p(stats), _p(w13), _p(w13_scale), _p(w_down), _p(w_down_scale), _p(w13_s),
-        _p(w13_s_scale), _p(w_down_s), _p(w_down_s_scale), _p(o), _p(ws), _s(stream)),
+    T, D, K, F = cfg.T, cfg.D, cfg.K, cfg.F
+    E = cfg.n_local_experts or cfg.E
+    z = moe_get_sizes(cfg)
+    R, i32, i8, f32, bf16 = (int(z.rows_max), torch.int32, torch.int8, torch.float32,
+                             torch.bfloat16)
+    if ws is not None and ws.numel() < moe_expert_ffn_i8_ws_bytes(cfg):
+        raise MoEError("moe_expert_ffn_i8: the workspace is too small")
+    check(lib().moe_expert_ffn_i8(ctypes.byref(cfg), *_args(
+        "moe_expert_ffn_i8", stream, ("x", x, bf16, T * D), ("offsets", offsets, i32, E + 2),
+        ("slot_row", slot_row, i32, T * K), ("row_slot", row_slot, i32, R),
+        ("tile_expert", tile_expert, i32, int(z.tiles_max)), ("stats", stats, i32, 4),
+        ("w13", w13, i8, E * 2 * F * D), ("w13_scale", w13_scale, f32, E * 2 * F),
+        ("w_down", w_down, i8, E * D * F), ("w_down_scale", w_down_scale, f32, E * D),
+        ("w13_s", w13_s, i8, 2 * F * D), ("w13_s_scale", w13_s_scale, f32, 2 * F),
+        ("w_down_s", w_down_s, i8, D * F), ("w_down_s_scale", w_down_s_scale, f32, D),
+        ("o", o, bf16, R * D), ("ws", ws, torch.uint8, 0 if ws is None else ws.numel()))),
         "moe_expert_ffn_i8")
 
 

@@ -132,20 +132,29 @@ quant_rows_kernel(const TX* x, int64_t rows, int cols, int64_t ld, int8_t* q, fl
 // to every row that holds the token (its slots' rows, the shared expert's).
 // The blocks behind the last token count the rows in use of each 128-row
 // tile: a routed expert's rows are a prefix of its segment, so the tile's
-// count is that of its non-negative row slots.
+// count is that of its non-negative row slots.  For experts of few rows
+// one more block per block of the gate/up product brings that one's first
+// weights into L2 (from one SM its copy engine would take 100 us).
 template <int NV>
 __global__ void __launch_bounds__(kQThreads)
-quant_dispatch_kernel(const __nv_bfloat16* x, int T, int D, int K, int E, int n_shared,
+quant_dispatch_kernel(const __grid_constant__ CUtensorMap mapW,
+                      const __grid_constant__ CUtensorMap mapWs, const i8::Ahead next,
+                      const int32_t* tile_expert, const __nv_bfloat16* x, int T, int D, int K, int E, int n_shared,
                       const int32_t* offsets, const int32_t* slot_row, const int32_t* row_slot,
-                      const int32_t* stats, int token_blocks, int8_t* xq, float* scale,
+                      const int32_t* stats, int token_blocks, int tile_blocks, int8_t* xq, float* scale,
                       unsigned* row_max, int32_t* tile_rows) {
   __shared__ unsigned red[kQThreads / 32];
   const int lane = threadIdx.x & 31;
   pdl_begin();
+  if ((int)blockIdx.x >= token_blocks + tile_blocks) {
+    if (threadIdx.x == 0)
+      next.bring(&mapW, &mapWs, tile_expert, stats[3], blockIdx.x - token_blocks - tile_blocks);
+    return;
+  }
   if ((int)blockIdx.x >= token_blocks) {
     const int warp = threadIdx.x >> 5;
     const int n_tiles = stats[3], shared0 = offsets[E] / kRowTile;
-    const int step = (gridDim.x - token_blocks) * (kQThreads >> 5);
+    const int step = tile_blocks * (kQThreads >> 5);
     for (int t = (blockIdx.x - token_blocks) * (kQThreads >> 5) + warp; t < n_tiles; t += step) {
       int n = 0;
       if (t >= shared0) {
@@ -255,7 +264,7 @@ int run_gemm(const char* name, const CUtensorMap& a, const CUtensorMap& b, const
              const CUtensorMap& o, const i8::Params& p, int64_t units, cudaStream_t s) {
   using S = i8::Smem<BN, ST, PAIR>;
   auto k = i8::gemm_i8_kernel<BN, ST, EPI, PAIR>;
-  MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes));
+  MOE_HTRY(host::allow_smem(k, S::kBytes));
   int64_t resident = host::sm_count();
   if (PAIR) MOE_HTRY(host::resident_clusters(k, 2, tc::kThreads, S::kBytes, &resident));
   const int ctas = (int)std::min<int64_t>(resident, units * p.nN) * (PAIR ? 2 : 1);
@@ -274,6 +283,42 @@ bool few_rows(const moe_config_t* c, const Work& w) {
   return (int64_t)c->T * c->K <= 32ll * w.v.local_experts;
 }
 
+// Maps and shape of one thin product's weights.
+struct ThinWeights {
+  CUtensorMap w, ws;
+  i8::Ahead a;
+};
+template <int EPI>
+int thin_weights(const moe_config_t* c, const Work& w, const int8_t* b, const int8_t* b_s,
+                 ThinWeights* t) {
+  constexpr uint32_t box = EPI == i8::I8_SWIGLU ? 64 : 128;
+  const int64_t cols = EPI == i8::I8_SWIGLU ? 2 * (int64_t)c->F : c->D;
+  const int64_t K = EPI == i8::I8_SWIGLU ? c->D : c->F;
+  t->a.E = w.v.local_experts;
+  t->a.F = EPI == i8::I8_SWIGLU ? c->F : 0;
+  t->a.nN = (EPI == i8::I8_SWIGLU ? c->F : c->D) / (int)box;
+  t->a.nk = (int)(K / i8::kBK);
+  t->a.ctas = (int)std::min<int64_t>(host::sm_count(), w.v.tiles_max * t->a.nN);
+  MOE_HTRY(host::make_map_u8(&t->w, b, w.v.local_experts, cols, K, box));
+  return host::make_map_u8(&t->ws, b_s != nullptr ? b_s : b, 1, cols, K, box);
+}
+
+template <int EPI>
+int thin_product(const Work& w, const char* name, const int8_t* a, const ThinWeights& t,
+                 const ThinWeights& next, void* out, i8::Params p, cudaStream_t s) {
+  auto k = i8::gemm_i8_thin_kernel<EPI>;
+  p.E = t.a.E; p.F = t.a.F; p.nk = t.a.nk; p.nN = t.a.nN;
+  p.cols = EPI == i8::I8_SWIGLU ? 2 * t.a.F : t.a.nN * 128;
+  CUtensorMap ma;
+  MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, (int64_t)t.a.nk * i8::kBK, 16));
+  i8::ThinParams tp{p, next.a, nullptr, nullptr};
+  if (EPI == i8::I8_SWIGLU) tp.h = static_cast<float*>(out);
+  else tp.o = static_cast<__nv_bfloat16*>(out);
+  MOE_HTRY(host::allow_smem(k, i8::ThinSmem::kBytes));
+  return host::launch(name, k, t.a.ctas, tc::kThreads, i8::ThinSmem::kBytes, s, 1, t.w, t.ws, ma,
+                      next.w, next.ws, tp);
+}
+
 template <int EPI>
 int product(const moe_config_t* c, const Work& w, const char* name, const int8_t* a, int64_t K,
             const int8_t* b, const int8_t* b_s, int64_t cols, void* out, i8::Params p,
@@ -282,32 +327,15 @@ int product(const moe_config_t* c, const Work& w, const char* name, const int8_t
   const int64_t n_out = EPI == i8::I8_SWIGLU ? c->F : c->D;
   const int64_t E = w.v.local_experts;
   p.E = (int)E; p.F = c->F; p.nk = (int)(K / i8::kBK); p.cols = (int)cols;
-  CUtensorMap ma, mb, mbs, mo;
-  auto weights = [&](uint32_t box) {
-    MOE_HTRY(host::make_map_u8(&mb, b, E, cols, K, box));
-    return host::make_map_u8(&mbs, b_s != nullptr ? b_s : b, 1, cols, K, box);
-  };
-  if (few_rows(c, w)) {
-    auto k = i8::gemm_i8_thin_kernel<EPI>;
-    constexpr uint32_t box = EPI == i8::I8_SWIGLU ? 64 : 128;
-    p.nN = (int)(n_out / box);
-    p.group_m = 1;
-    MOE_HTRY(weights(box));
-    MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, K, 16));
-    i8::ThinParams tp{p, nullptr, nullptr};
-    if (EPI == i8::I8_SWIGLU) tp.h = static_cast<float*>(out);
-    else tp.o = static_cast<__nv_bfloat16*>(out);
-    MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 i8::ThinSmem::kBytes));
-    const int ctas = (int)std::min<int64_t>(host::sm_count(), w.v.tiles_max * p.nN);
-    return host::launch(name, k, ctas, tc::kThreads, i8::ThinSmem::kBytes, s, 1, mb, mbs, ma, tp);
-  }
   // D and F are multiples of 128: a 256-wide plain tile may not divide D
   const int bn = EPI == i8::I8_STORE && n_out % 256 ? 128 : 256;
   p.nN = (int)(n_out / (EPI == i8::I8_SWIGLU ? bn / 2 : bn));
   p.group_m = group_rows(K, pair);
+  CUtensorMap ma, mb, mbs, mo;
+  const uint32_t box = (uint32_t)(EPI == i8::I8_SWIGLU || pair ? bn / 2 : bn);
   MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, K, 128));
-  MOE_HTRY(weights((uint32_t)(EPI == i8::I8_SWIGLU || pair ? bn / 2 : bn)));
+  MOE_HTRY(host::make_map_u8(&mb, b, E, cols, K, box));
+  MOE_HTRY(host::make_map_u8(&mbs, b_s != nullptr ? b_s : b, 1, cols, K, box));
   MOE_HTRY(host::make_out_map(&mo, out, w.v.rows_max, n_out, EPI == i8::I8_SWIGLU));
   const int64_t units = w.v.tiles_max / (pair ? 2 : 1);
   if (pair) {
@@ -395,14 +423,20 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
   unsigned* row_max = reinterpret_cast<unsigned*>(base + w.row_max);
   int32_t* tile_rows = reinterpret_cast<int32_t*>(base + w.tile_rows);
   const int sms = host::sm_count();
+  const bool thin = few_rows(c, w);
+  ThinWeights t13{}, td{};
+  if (thin) {
+    MOE_HTRY((thin_weights<i8::I8_SWIGLU>(c, w, w13, w13_s, &t13)));
+    MOE_HTRY((thin_weights<i8::I8_STORE>(c, w, w_down, w_down_s, &td)));
+  }
   {
     const int tokens = (int)std::min<int64_t>(c->T, (int64_t)sms * 16);
     const int tiles = (int)std::min<int64_t>(host::ceil_div(w.v.tiles_max, kQThreads / 32), 64);
     auto go = [&](auto k) {
-      return host::launch("quant_dispatch", k, tokens + tiles, kQThreads, 0, s, 1,
-                          static_cast<const __nv_bfloat16*>(x), c->T, c->D, c->K,
-                          w.v.local_experts, c->n_shared, offsets, slot_row, row_slot, stats,
-                          tokens, xq, xs, row_max, tile_rows);
+      return host::launch("quant_dispatch", k, tokens + tiles + t13.a.ctas, kQThreads, 0, s, 1, t13.w, t13.ws,
+                          t13.a, tile_expert, static_cast<const __nv_bfloat16*>(x), c->T, c->D,
+                          c->K, w.v.local_experts, c->n_shared, offsets, slot_row, row_slot, stats,
+                          tokens, tiles, xq, xs, row_max, tile_rows);
     };
     const int64_t nv = host::ceil_div(c->D, kQThreads * 16);
     if (nv <= 1) MOE_HTRY(go(quant_dispatch_kernel<1>));
@@ -410,18 +444,23 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
     else if (nv <= 4) MOE_HTRY(go(quant_dispatch_kernel<4>));
     else MOE_HTRY(go(quant_dispatch_kernel<0>));
   }
-  i8::Params p{};
+  i8::Params p{}, q{};
   p.tile_expert = tile_expert; p.tile_rows = tile_rows; p.stats = stats;
   p.row_scale = xs; p.row_max = row_max;
+  q = p;
   p.col_scale = w13_scale; p.col_scale_s = w13_s_scale;
-  MOE_HTRY((product<i8::I8_SWIGLU>(c, w, "i8_gate_up", xq, c->D, w13, w13_s, 2 * (int64_t)c->F, h,
-                                   p, s)));
+  q.col_scale = w_down_scale; q.col_scale_s = w_down_s_scale;
+  if (thin)
+    MOE_HTRY((thin_product<i8::I8_SWIGLU>(w, "i8_gate_up_thin", xq, t13, td, h, p, s)));
+  else
+    MOE_HTRY((product<i8::I8_SWIGLU>(c, w, "i8_gate_up", xq, c->D, w13, w13_s, 2 * (int64_t)c->F,
+                                     h, p, s)));
   MOE_HTRY(host::launch("quant_h", quant_h_kernel,
                         (int)std::min<int64_t>(host::ceil_div(w.v.rows_max * host::ceil_div(c->F, 512), 8),
                                                (int64_t)sms * 8),
                         kHThreads, 0, s, 1, h, c->F, stats, tile_rows, row_max, hq));
-  p.col_scale = w_down_scale; p.col_scale_s = w_down_s_scale;
-  return product<i8::I8_STORE>(c, w, "i8_down", hq, c->F, w_down, w_down_s, c->D, o, p, s);
+  if (thin) return thin_product<i8::I8_STORE>(w, "i8_down_thin", hq, td, td, o, q, s);
+  return product<i8::I8_STORE>(c, w, "i8_down", hq, c->F, w_down, w_down_s, c->D, o, q, s);
 }
 
 }  // extern "C"

@@ -452,8 +452,39 @@ __device__ __forceinline__ bool pair_and(int bar, bool v) {
   return r != 0;
 }
 
+// Asks for a box of a weight tensor to be brought into L2.
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+// A thin product that follows: what its blocks load first.  A decoded
+// token's kernels are short against DRAM's latency, so a kernel that has
+// issued its own loads brings the next product's first stages (at most 21 MB)
+// into L2 (one token on the OLMoE-shaped layer: XXX).
+struct Ahead {
+  int E, nN, nk, ctas, F;        // F > 0: gate and up rows of 64-channel tiles
+  __device__ __forceinline__ void bring(const CUtensorMap* w, const CUtensorMap* ws,
+                                        const int32_t* tile_expert, int n_mt, int b) const {
+    if (b >= min(ctas, n_mt * nN)) return;
+    const int e = __ldcg(tile_expert + b / nN), nt = b % nN;
+    const CUtensorMap* m = e >= E ? ws : w;
+    const int c2 = e >= E ? 0 : e;
+    for (int k = 0; k < min(nk, kThinStages - 1); ++k) {
+      if (F > 0) {
+        prefetch_3d(m, k * kBK, nt * 64, c2);
+        prefetch_3d(m, k * kBK, F + nt * 64, c2);
+      } else {
+        prefetch_3d(m, k * kBK, nt * 128, c2);
+      }
+    }
+  }
+};
+
 struct ThinParams {
   Params p;
+  Ahead next;                    // I8_SWIGLU: the down product
   float* h;                      // I8_SWIGLU out [rows_max, F]
   __nv_bfloat16* o;              // I8_STORE out [rows_max, cols]
 };
@@ -462,7 +493,9 @@ template <int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
                     const __grid_constant__ CUtensorMap mapWs,
-                    const __grid_constant__ CUtensorMap mapT, const ThinParams tp) {
+                    const __grid_constant__ CUtensorMap mapT,
+                    const __grid_constant__ CUtensorMap mapN,
+                    const __grid_constant__ CUtensorMap mapNs, const ThinParams tp) {
   using S = ThinSmem;
   const Params& p = tp.p;
   constexpr int STAGES = thin_stages<EPI>(), NACC = S::NACC;
@@ -519,10 +552,7 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
   };
   auto decode_at = [&](int t) {
     if (t >= total) return T{0, 0, 0, 0};
-    // row tiles of one expert are neighbours and share its weights' columns
-    const int group = t / (p.group_m * p.nN), first = group * p.group_m;
-    const int gm = min(p.group_m, n_mt - first), local = t - group * p.group_m * p.nN;
-    const int mt = first + local % gm, nt = local / gm;
+    const int mt = t / p.nN, nt = t - mt * p.nN;
     // (a tile in use holds a row; one without would leave requested weights
     // unused)
     return T{__ldcg(p.tile_expert + mt), mt * BM, nt * kCh, max(1, __ldcg(p.tile_rows + mt))};
@@ -540,9 +570,7 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
   int early = 0;
   if (warp == 0 && lane == 0 && (int)blockIdx.x < total) {
     const int t = blockIdx.x;
-    const int group = t / (p.group_m * p.nN), first = group * p.group_m;
-    const int gm = min(p.group_m, n_mt - first), local = t - group * p.group_m * p.nN;
-    const int e = __ldcg(p.tile_expert + first + local % gm), n0 = local / gm * kCh;
+    const int e = __ldcg(p.tile_expert + t / p.nN), n0 = t % p.nN * kCh;
     early = min(STAGES, p.nk);
     for (int s = 0; s < early; ++s) {
       mbar_expect_only(full_bar(s), S::kA);
@@ -587,6 +615,9 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
           }
         }
       }
+      if (EPI == I8_SWIGLU)
+        for (int b = blockIdx.x; b < tp.next.ctas; b += gridDim.x)
+          tp.next.bring(&mapN, &mapNs, p.tile_expert, n_mt, b);
       for (int s = 0; s < STAGES; ++s)
         if (issued_parity[s] >= 0) mbar_wait(full_bar(s), (uint32_t)issued_parity[s], abort_flag);
     }

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <cstdint>
 #include <utility>
 
 #include "common.cuh"
@@ -79,6 +80,26 @@ int launch(const char* name, void (*kern)(KP...), dim3 grid, dim3 block, size_t 
   before_launch(s);
   MOE_HCK(cudaLaunchKernelEx(&lc, kern, std::forward<A>(args)...));
   return after_launch(s, name);
+}
+
+// Raises a kernel's dynamic shared-memory limit, once per device and kernel
+// (the call costs as much as a fifth of a launch).
+template <typename K>
+int allow_smem(K k, int bytes) {
+  struct Seen {
+    const void* fn;
+    uint64_t devices;
+  };
+  static thread_local Seen seen[64];
+  int dev = 0;
+  MOE_HCK(cudaGetDevice(&dev));
+  const void* fn = reinterpret_cast<const void*>(k);
+  Seen& at = seen[(reinterpret_cast<uintptr_t>(fn) >> 4) % 64];
+  if (at.fn != fn) at = Seen{fn, 0};
+  if (dev < 64 && (at.devices >> dev) & 1) return MOE_OK;
+  MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  if (dev < 64) at.devices |= 1ull << dev;
+  return MOE_OK;
 }
 
 // Clusters of `size` CTAs of kernel k that the current device holds at once.

@@ -2185,7 +2185,13 @@ int after_launch(cudaStream_t s, const char* name) {
   return MOE_OK;
 }
 bool use_pdl() { return pdl_enabled(); }
-int sm_count() { return num_sms(); }
+int sm_count() {
+  static thread_local int known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms();
+  if (known[dev] == 0) known[dev] = num_sms();
+  return known[dev];
+}
 
 int make_map_u8(CUtensorMap* m, const void* ptr, int64_t n3, int64_t rows, int64_t cols,
                 uint32_t box_rows) {

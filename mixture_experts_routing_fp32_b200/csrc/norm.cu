@@ -649,7 +649,7 @@ int forward(NormArgs a, cudaStream_t s) {
   const int grid = (int)std::min<int64_t>(host::ceil_div(a.T, a.R), (int64_t)sms * per_sm);
   return with_flags(bias, a.D % 256 == 0, [&](auto b, auto f) {
     auto k = block_norm_kernel<TA, TR, decltype(b)::value, decltype(f)::value>;
-    MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem));
+    MOE_HTRY(host::allow_smem(k, kDynSmem));
     return host::launch("block_norm", k, grid, threads, smem, s, 1, a);
   });
 }
@@ -670,7 +670,7 @@ int backward(NormArgs a, int P, bool bias, SumArgs& sum, cudaStream_t s) {
   if (a.stages < 2) a.stages = 0;
   const size_t smem = a.stages * stage + fixed;
   auto go = [&](auto k) {
-    MOE_HCK(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem));
+    MOE_HTRY(host::allow_smem(k, kDynSmem));
     return host::launch("block_norm_bwd", k, P, threads, smem, s, 1, a);
   };
   MOE_HTRY(with_flags(general, a.several != 0, [&](auto ge, auto se) {

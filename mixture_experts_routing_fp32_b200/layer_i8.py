@@ -73,9 +73,9 @@ class MoEInt8Layer:
                 continue
             for t, want, dt in ((q, shape, torch.int8), (s, shape[:-1], torch.float32)):
                 if (t is None or tuple(t.shape) != want or t.dtype != dt or not t.is_contiguous()
-                        or t.device.type != "cuda"):
-                    raise MoEError("set_weights: %s is not a contiguous CUDA tensor of %s %s"
-                                   % (k, want, dt))
+                        or t.device != self.y.device):
+                    raise MoEError("set_weights: %s is not a contiguous tensor of %s %s on %s"
+                                   % (k, want, dt, self.y.device))
             kept += [q, s]
         self.weights = tuple(kept)
         self._w = [api._p(t) for t in kept]
@@ -98,17 +98,19 @@ class MoEInt8Layer:
         [T, K] fp32): the layer's own buffer, rewritten by the next call."""
         if self.weights is None:
             raise MoEError("MoEInt8Layer: no weights (set_weights or quantize first)")
-        c, P, L = self.cfg, api._p, lib()
-        for t, shape, dt in ((x, (c.T, c.D), torch.bfloat16), (topk_idx, (c.T, c.K), torch.int32),
-                             (topk_w, (c.T, c.K), torch.float32)):
-            if t.shape != shape or t.dtype != dt or not t.is_contiguous():
-                raise MoEError("MoEInt8Layer: expected a contiguous %s tensor of %s" % (shape, dt))
-        s, xp = api._s(), P(x)
-        check(L.moe_dispatch(self._cfg_p, P(topk_idx), P(sentinel_mask), xp, *self._layout, None,
-                             self._ws, s), "moe_dispatch")
+        c, L = self.cfg, lib()
+        xp, idx, w, mask, s = api._args(
+            "MoEInt8Layer", None, ("x", x, torch.bfloat16, c.T * c.D),
+            ("topk_idx", topk_idx, torch.int32, c.T * c.K),
+            ("topk_w", topk_w, torch.float32, c.T * c.K),
+            ("sentinel_mask", sentinel_mask, torch.uint8, c.T * c.K))
+        if self.y.get_device() != x.get_device():
+            raise MoEError("MoEInt8Layer: the layer is on %s, x on %s" % (self.device, x.device))
+        check(L.moe_dispatch(self._cfg_p, idx, mask, xp, *self._layout, None, self._ws, s),
+              "moe_dispatch")
         check(L.moe_expert_ffn_i8(self._cfg_p, xp, *self._map, *self._w, self._o, self._ws_i8, s),
               "moe_expert_ffn_i8")
-        check(L.moe_combine(self._cfg_p, self._o, self._slots, P(topk_w), self._off, self._y, s),
+        check(L.moe_combine(self._cfg_p, self._o, self._slots, w, self._off, self._y, s),
               "moe_combine")
         return self.y
 

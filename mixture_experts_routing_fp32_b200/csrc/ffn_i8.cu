@@ -290,33 +290,47 @@ struct ThinWeights {
 };
 template <int EPI>
 int thin_weights(const moe_config_t* c, const Work& w, const int8_t* b, const int8_t* b_s,
-                 ThinWeights* t) {
+                 int stages, ThinWeights* t) {
   constexpr uint32_t box = EPI == i8::I8_SWIGLU ? 64 : 128;
-  const int64_t cols = EPI == i8::I8_SWIGLU ? 2 * (int64_t)c->F : c->D;
   const int64_t K = EPI == i8::I8_SWIGLU ? c->D : c->F;
   t->a.E = w.v.local_experts;
-  t->a.F = EPI == i8::I8_SWIGLU ? c->F : 0;
+  t->a.ch = (int)box;
   t->a.nN = (EPI == i8::I8_SWIGLU ? c->F : c->D) / (int)box;
   t->a.nk = (int)(K / i8::kBK);
   t->a.ctas = (int)std::min<int64_t>(host::sm_count(), w.v.tiles_max * t->a.nN);
-  MOE_HTRY(host::make_map_u8(&t->w, b, w.v.local_experts, cols, K, box));
-  return host::make_map_u8(&t->ws, b_s != nullptr ? b_s : b, 1, cols, K, box);
+  const int64_t halves = EPI == i8::I8_SWIGLU ? 2 : 1, rows = EPI == i8::I8_SWIGLU ? c->F : c->D;
+  t->a.stages = stages;
+  MOE_HTRY(host::make_map_k(&t->w, b, w.v.local_experts, halves, rows, K, box, (uint32_t)halves,
+                            i8::kThinKb));
+  return host::make_map_k(&t->ws, b_s != nullptr ? b_s : b, 1, halves, rows, K, box,
+                          (uint32_t)halves, i8::kThinKb);
 }
 
-template <int EPI>
+template <int EPI, int NT>
 int thin_product(const Work& w, const char* name, const int8_t* a, const ThinWeights& t,
                  const ThinWeights& next, void* out, i8::Params p, cudaStream_t s) {
-  auto k = i8::gemm_i8_thin_kernel<EPI>;
-  p.E = t.a.E; p.F = t.a.F; p.nk = t.a.nk; p.nN = t.a.nN;
-  p.cols = EPI == i8::I8_SWIGLU ? 2 * t.a.F : t.a.nN * 128;
+  auto k = i8::gemm_i8_thin_kernel<EPI, NT>;
+  p.E = t.a.E; p.F = EPI == i8::I8_SWIGLU ? t.a.nN * t.a.ch : 0; p.nk = t.a.nk; p.nN = t.a.nN;
+  p.cols = EPI == i8::I8_SWIGLU ? 2 * p.F : t.a.nN * t.a.ch;
   CUtensorMap ma;
-  MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, (int64_t)t.a.nk * i8::kBK, 16));
+  MOE_HTRY(host::make_map_k(&ma, a, 1, 1, w.v.rows_max, (int64_t)t.a.nk * i8::kBK, NT, 1,
+                            i8::kThinKb));
   i8::ThinParams tp{p, next.a, nullptr, nullptr};
   if (EPI == i8::I8_SWIGLU) tp.h = static_cast<float*>(out);
   else tp.o = static_cast<__nv_bfloat16*>(out);
-  MOE_HTRY(host::allow_smem(k, i8::ThinSmem::kBytes));
-  return host::launch(name, k, t.a.ctas, tc::kThreads, i8::ThinSmem::kBytes, s, 1, t.w, t.ws, ma,
-                      next.w, next.ws, tp);
+  constexpr int bytes = i8::ThinSmem<NT>::kBytes;
+  MOE_HTRY(host::allow_smem(k, bytes));
+  return host::launch(name, k, t.a.ctas, tc::kThreads, bytes, s, 1, t.w, t.ws, ma, next.w, next.ws,
+                      tp);
+}
+// Tokens of an MMA: an expert holds a token once, so T tokens need no more
+// than T rows.
+int thin_tokens(const moe_config_t* c) { return c->T <= 16 ? 16 : c->T <= 32 ? 32 : 64; }
+template <int EPI, typename... A>
+int thin_product_of(int nt, A&&... args) {
+  if (nt == 16) return thin_product<EPI, 16>(std::forward<A>(args)...);
+  if (nt == 32) return thin_product<EPI, 32>(std::forward<A>(args)...);
+  return thin_product<EPI, 64>(std::forward<A>(args)...);
 }
 
 template <int EPI>
@@ -332,19 +346,22 @@ int product(const moe_config_t* c, const Work& w, const char* name, const int8_t
   p.nN = (int)(n_out / (EPI == i8::I8_SWIGLU ? bn / 2 : bn));
   p.group_m = group_rows(K, pair);
   CUtensorMap ma, mb, mbs, mo;
-  const uint32_t box = (uint32_t)(EPI == i8::I8_SWIGLU || pair ? bn / 2 : bn);
-  MOE_HTRY(host::make_map_u8(&ma, a, 1, w.v.rows_max, K, 128));
-  MOE_HTRY(host::make_map_u8(&mb, b, E, cols, K, box));
-  MOE_HTRY(host::make_map_u8(&mbs, b_s != nullptr ? b_s : b, 1, cols, K, box));
+  const bool sw = EPI == i8::I8_SWIGLU;
+  const uint32_t kb = pair || bn == 128 ? 2 : 1;     // i8::kKb
+  const uint32_t box = (uint32_t)(sw || pair ? bn / 2 : bn), halves = sw && !pair ? 2 : 1;
+  const int64_t rows = sw ? cols / 2 : cols;
+  MOE_HTRY(host::make_map_k(&ma, a, 1, 1, w.v.rows_max, K, 128, 1, kb));
+  MOE_HTRY(host::make_map_k(&mb, b, E, sw ? 2 : 1, rows, K, box, halves, kb));
+  MOE_HTRY(host::make_map_k(&mbs, b_s != nullptr ? b_s : b, 1, sw ? 2 : 1, rows, K, box, halves, kb));
   MOE_HTRY(host::make_out_map(&mo, out, w.v.rows_max, n_out, EPI == i8::I8_SWIGLU));
   const int64_t units = w.v.tiles_max / (pair ? 2 : 1);
   if (pair) {
-    if (bn == 256) return run_gemm<256, 5, EPI, true>(name, ma, mb, mbs, mo, p, units, s);
+    if (bn == 256) return run_gemm<256, 3, EPI, true>(name, ma, mb, mbs, mo, p, units, s);
     if constexpr (EPI == i8::I8_STORE)
-      return run_gemm<128, 6, EPI, true>(name, ma, mb, mbs, mo, p, units, s);
+      return run_gemm<128, 4, EPI, true>(name, ma, mb, mbs, mo, p, units, s);
   }
   if constexpr (EPI == i8::I8_STORE) {
-    if (bn == 128) return run_gemm<128, 5, EPI, false>(name, ma, mb, mbs, mo, p, units, s);
+    if (bn == 128) return run_gemm<128, 3, EPI, false>(name, ma, mb, mbs, mo, p, units, s);
   }
   return run_gemm<256, 4, EPI, false>(name, ma, mb, mbs, mo, p, units, s);
 }
@@ -424,10 +441,13 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
   int32_t* tile_rows = reinterpret_cast<int32_t*>(base + w.tile_rows);
   const int sms = host::sm_count();
   const bool thin = few_rows(c, w);
+  const int nt = thin_tokens(c);
   ThinWeights t13{}, td{};
   if (thin) {
-    MOE_HTRY((thin_weights<i8::I8_SWIGLU>(c, w, w13, w13_s, &t13)));
-    MOE_HTRY((thin_weights<i8::I8_STORE>(c, w, w_down, w_down_s, &td)));
+    const int st = nt == 16 ? i8::ThinSmem<16>::kStages
+                   : nt == 32 ? i8::ThinSmem<32>::kStages : i8::ThinSmem<64>::kStages;
+    MOE_HTRY((thin_weights<i8::I8_SWIGLU>(c, w, w13, w13_s, st, &t13)));
+    MOE_HTRY((thin_weights<i8::I8_STORE>(c, w, w_down, w_down_s, st, &td)));
   }
   {
     const int tokens = (int)std::min<int64_t>(c->T, (int64_t)sms * 16);
@@ -451,7 +471,7 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
   p.col_scale = w13_scale; p.col_scale_s = w13_s_scale;
   q.col_scale = w_down_scale; q.col_scale_s = w_down_s_scale;
   if (thin)
-    MOE_HTRY((thin_product<i8::I8_SWIGLU>(w, "i8_gate_up_thin", xq, t13, td, h, p, s)));
+    MOE_HTRY((thin_product_of<i8::I8_SWIGLU>(nt, w, "i8_gate_up_thin", xq, t13, td, h, p, s)));
   else
     MOE_HTRY((product<i8::I8_SWIGLU>(c, w, "i8_gate_up", xq, c->D, w13, w13_s, 2 * (int64_t)c->F,
                                      h, p, s)));
@@ -459,7 +479,7 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
                         (int)std::min<int64_t>(host::ceil_div(w.v.rows_max * host::ceil_div(c->F, 512), 8),
                                                (int64_t)sms * 8),
                         kHThreads, 0, s, 1, h, c->F, stats, tile_rows, row_max, hq));
-  if (thin) return thin_product<i8::I8_STORE>(w, "i8_down_thin", hq, td, td, o, q, s);
+  if (thin) return thin_product_of<i8::I8_STORE>(nt, w, "i8_down_thin", hq, td, td, o, q, s);
   return product<i8::I8_STORE>(c, w, "i8_down", hq, c->F, w_down, w_down_s, c->D, o, q, s);
 }
 

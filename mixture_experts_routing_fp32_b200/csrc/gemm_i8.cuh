@@ -60,22 +60,29 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void tma_3d_pair_hint(uint32_t dst, const CUtensorMap* map,
-                                                 uint32_t bar, int c0, int c1, int c2,
-                                                 uint64_t pol) {
+// Loads of host::make_map_k boxes: k block kb, rows from r, half h, matrix e.
+__device__ __forceinline__ void tma_k(uint32_t dst, const CUtensorMap* map, uint32_t bar, int kb,
+                                      int r, int h, int e, uint64_t pol) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(pol)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(r), "r"(h), "r"(kb), "r"(e), "r"(bar),
+      "l"(pol)
       : "memory");
 }
-__device__ __forceinline__ void tma_3d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int c0, int c1, int c2, uint64_t pol) {
+__device__ __forceinline__ void tma_k_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                           int kb, int r, int h, int e, uint64_t pol) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(pol)
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(r), "r"(h), "r"(kb), "r"(e), "r"(bar),
+      "l"(pol)
       : "memory");
+}
+__device__ __forceinline__ uint64_t policy_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 
 // Scale of a row from the bits of its largest |h|; NaN when that is not
@@ -84,13 +91,21 @@ __device__ __forceinline__ float scale_of(unsigned bits) {
   return bits >= 0x7f800000u ? __int_as_float(0x7fffffff) : __uint_as_float(bits) / 127.0f;
 }
 
+// KB k blocks to a stage, each operand's by one copy: the producer thread
+// needs about 350 ns for a stage's wait, arming and copies, whatever they
+// move.  Pair tiles and 128-wide ones take two (64 KB and 48-64 KB stages);
+// two 96 KB stages of the 256-wide single tile would be too few.
+template <int BN, bool PAIR>
+constexpr int kKb = (PAIR || BN == 128) ? 2 : 1;
+
 template <int BN, int STAGES, bool PAIR>
 struct Smem {
+  static constexpr int KB = kKb<BN, PAIR>;
   static constexpr int BNC = PAIR ? BN / 2 : BN;      // columns of B this CTA holds
   static constexpr int NACC = BN <= 128 ? 4 : 2;
   static constexpr int kA = BM * kBK;
   static constexpr int kB = BNC * kBK;
-  static constexpr int kStage = kA + kB;
+  static constexpr int kStage = KB * (kA + kB);       // [A of each k block | B of each]
   static constexpr int kBars = (2 * STAGES + 2 * NACC + 1) * 8;
   static constexpr int kEpiOff = (STAGES * kStage + kBars + 16 + 1023) / 1024 * 1024;
   static constexpr int kStgW = 4096;                  // one 32 x 32 fp32 box, or two bf16 boxes
@@ -118,14 +133,14 @@ __device__ __forceinline__ Tile8 decode8(int t, const Params& p, int rank, int n
   return d;
 }
 
-// mapA: [rows_max][K]; mapB / mapBs: [E][cols][K] (the shared expert's own); mapO: h [rows_max][F]
+// mapA: [rows_max][K]; mapB / mapBs: [E][halves][cols][K] (the shared expert's own); mapO: h [rows_max][F]
 // fp32, or o [rows_max][D] bf16, for the epilogue's TMA stores.
 template <int BN, int STAGES, int EPI, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapBs,
                const __grid_constant__ CUtensorMap mapO, const Params p) {
   using S = Smem<BN, STAGES, PAIR>;
-  constexpr int NACC = S::NACC;
+  constexpr int NACC = S::NACC, KB = S::KB;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   volatile int* abort_flag = &abort_flag_s;
@@ -194,7 +209,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer (both CTAs of a pair) ----------------
-      const uint64_t pol_a = policy_evict_last();
+      const uint64_t pol_a = policy_evict_last(), pol_b = policy_normal();
       int stage = 0;
       uint32_t phase = 0;
       int issued_parity[STAGES];
@@ -207,28 +222,22 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
         nxt = decode_at(t + n_units);
         const CUtensorMap* mb = d.e >= p.E ? &mapBs : &mapB;
         const int eb = d.e >= p.E ? 0 : d.e;
-        for (int kb = 0; kb < p.nk; ++kb) {
+        for (int kb = 0; kb < p.nk; kb += KB) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = base + stage * S::kStage;
-          const uint32_t sb = sa + S::kA;
+          const uint32_t sb = sa + KB * S::kA;
           const uint32_t fb = full_bar(stage);
-          if (!PAIR || leader) mbar_expect_tx(fb, (PAIR ? 2 : 1) * (S::kA + S::kB));
+          if (!PAIR || leader) mbar_expect_tx(fb, (PAIR ? 2 : 1) * S::kStage);
           issued_parity[stage] = (int)phase;
-          const int k0 = kb * kBK;
           if constexpr (PAIR) {
             const uint32_t lfb = mapa(fb, 0);
-            tma_3d_pair_hint(sa, &mapA, lfb, k0, d.m0, 0, pol_a);
+            tma_k_pair(sa, &mapA, lfb, kb, d.m0, 0, 0, pol_a);
             // SwiGLU: this CTA holds the gate (rank 0) or the up (rank 1) rows
-            tma_3d_pair(sb, mb, lfb, k0,
-                        EPI == I8_SWIGLU ? (rank ? p.F : 0) + d.n0 : d.n0 + rank * (BN / 2), eb);
+            tma_k_pair(sb, mb, lfb, kb, EPI == I8_SWIGLU ? d.n0 : d.n0 + rank * (BN / 2),
+                       EPI == I8_SWIGLU ? rank : 0, eb, pol_b);
           } else {
-            tma_3d_hint(sa, &mapA, fb, k0, d.m0, 0, pol_a);
-            if (EPI == I8_SWIGLU) {
-              tma_3d(sb, mb, fb, k0, d.n0, eb);
-              tma_3d(sb + (BN / 2) * kBK, mb, fb, k0, p.F + d.n0, eb);
-            } else {
-              tma_3d(sb, mb, fb, k0, d.n0, eb);
-            }
+            tma_k(sa, &mapA, fb, kb, d.m0, 0, 0, pol_a);
+            tma_k(sb, mb, fb, kb, d.n0, 0, eb, pol_b);   // (SwiGLU: gate and up rows)
           }
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -251,17 +260,20 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
         if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t dt = tmem + acc * BN;
-        for (int kb = 0; kb < p.nk; ++kb) {
+        for (int kb = 0; kb < p.nk; kb += KB) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = base + stage * S::kStage;
-          const uint32_t sb = sa + S::kA;
 #pragma unroll
-          for (int ks = 0; ks < kBK / kUmmaK; ++ks) {
-            const uint64_t ad = sw128_desc(sa + ks * kUmmaK, 16, 1024);
-            const uint64_t bd = sw128_desc(sb + ks * kUmmaK, 16, 1024);
-            if constexpr (PAIR) umma_i8_pair(dt, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
-            else umma_i8(dt, ad, bd, idesc, (kb | ks) != 0 ? 1u : 0u);
+          for (int j = 0; j < KB; ++j) {      // (a block past the last holds zeros)
+            const uint32_t sa = base + stage * S::kStage + j * S::kA;
+            const uint32_t sb = base + stage * S::kStage + KB * S::kA + j * S::kB;
+#pragma unroll
+            for (int ks = 0; ks < kBK / kUmmaK; ++ks) {
+              const uint64_t ad = sw128_desc(sa + ks * kUmmaK, 16, 1024);
+              const uint64_t bd = sw128_desc(sb + ks * kUmmaK, 16, 1024);
+              if constexpr (PAIR) umma_i8_pair(dt, ad, bd, idesc, (kb | j | ks) != 0 ? 1u : 0u);
+              else umma_i8(dt, ad, bd, idesc, (kb | j | ks) != 0 ? 1u : 0u);
+            }
           }
           if constexpr (PAIR) umma_commit_pair_both(empty_bar(stage));
           else umma_commit(empty_bar(stage));
@@ -405,36 +417,38 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
 // ---------------------------------------------------------------------------
 // With a handful of tokens per expert a product is bound by reading its
 // weights once, so the operands change places: 128 weight rows are the MMA's
-// M side and the tokens its N side (16 to 64 of them, in steps of 16), and of
-// a stage's bytes all but the tokens' few are weights.  Nine stages of 16 KB
-// keep 144 KB of weights in flight per SM: under full load a copy takes
-// about 3 us from issue to arrival here, so DRAM's rate needs some 20 MB in
-// flight over the 148 SMs (the general kernel's narrow tiles held 8 MB and
-// read the Mixtral-shaped down projection at 2.7 TB/s).
+// M side and NT = 16, 32 or 64 tokens its N side, and of a stage's bytes all
+// but the tokens' few are weights.  A stage holds two k blocks, each
+// operand's brought by one copy, and the stages together 128 to 192 KB of
+// weights per SM: under full load a copy takes about 3 us from issue to
+// arrival here, so DRAM's rate needs some 20 MB in flight over the 148 SMs
+// (the general kernel's narrow tiles held 8 MB and read the Mixtral-shaped
+// down projection at 2.7 TB/s), and the producer thread needs about 350 ns
+// for a stage, which held stages of 16 KB to 45 GB/s per SM.
 //
 // Accumulators are [channel][token]: a lane owns a channel, so a token's
 // outputs leave as coalesced 32-lane rows.  A gate/up tile holds 64 gate
 // rows (lanes 0-63) and the 64 up rows of the same channels (lanes 64-127);
-// the up warps pass their values through shared memory.  More than 64 tokens
+// the up warps pass their values through shared memory.  More than NT tokens
 // in a 128-row tile run in turns over the same weights (the second turn
 // reads them from L2).
-constexpr int kThinTok = 64;
-constexpr int kThinStages = 9;
+constexpr int kThinKb = 2;
+template <int NT>
 struct ThinSmem {
   static constexpr int kA = 128 * kBK;
-  static constexpr int kB = kThinTok * kBK;
-  static constexpr int kStage = kA + kB;
+  static constexpr int kB = NT * kBK;
+  static constexpr int kStage = kThinKb * (kA + kB);
+  static constexpr int kStages = NT == 16 ? 6 : NT == 32 ? 5 : 4;
   static constexpr int NACC = 4;
-  static constexpr int kBars = (2 * kThinStages + 2 * NACC + 1) * 8;
-  static constexpr int kEpiOff = (kThinStages * kStage + kBars + 16 + 127) / 128 * 128;
-  // the gate/up form's exchange buffer, [pair of warps][token][channel]
-  // fp32, replaces its ninth stage
-  static_assert(4 * 32 * 32 * 4 <= kStage, "exchange buffer");
-  static constexpr int kBytes = 1024 + kEpiOff;
+  static constexpr int kAccCols = NT < 32 ? 32 : NT;     // columns of an accumulator
+  static constexpr int kHalves = NT > 32 ? 2 : 1;        // 32-token halves of a turn
+  static constexpr int kBars = (2 * kStages + 2 * NACC + 1) * 8;
+  // the gate/up form's exchange buffer, [pair of warps][token][channel] fp32
+  static constexpr int kSwapOff = kStages * kStage;
+  static constexpr int kBarOff = kSwapOff + 2 * kHalves * 32 * 32 * 4;
+  static constexpr int kBytes = 1024 + kBarOff + kBars + 16;
   static_assert(kBytes <= 232448 - 64, "shared memory per CTA");
 };
-template <int EPI> constexpr int thin_stages() { return EPI == I8_SWIGLU ? 8 : kThinStages; }
-
 // Bytes to come on `bar`, without an arrival.
 __device__ __forceinline__ void mbar_expect_only(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
@@ -453,32 +467,24 @@ __device__ __forceinline__ bool pair_and(int bar, bool v) {
 }
 
 // Asks for a box of a weight tensor to be brought into L2.
-__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+__device__ __forceinline__ void prefetch_k(const CUtensorMap* map, int kb, int r, int e) {
+  asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1), "r"(c2)
+               "r"(0), "r"(r), "r"(0), "r"(kb), "r"(e)
                : "memory");
 }
 // A thin product that follows: what its blocks load first.  A decoded
 // token's kernels are short against DRAM's latency, so a kernel that has
-// issued its own loads brings the next product's first stages (at most 21 MB)
-// into L2 (one token on the OLMoE-shaped layer: XXX).
+// issued its own loads brings the next product's first stages (at most 28 MB)
+// into L2.
 struct Ahead {
-  int E, nN, nk, ctas, F;        // F > 0: gate and up rows of 64-channel tiles
+  int E, nN, nk, ctas, ch, stages;       // ch: channels of a tile
   __device__ __forceinline__ void bring(const CUtensorMap* w, const CUtensorMap* ws,
                                         const int32_t* tile_expert, int n_mt, int b) const {
     if (b >= min(ctas, n_mt * nN)) return;
-    const int e = __ldcg(tile_expert + b / nN), nt = b % nN;
-    const CUtensorMap* m = e >= E ? ws : w;
-    const int c2 = e >= E ? 0 : e;
-    for (int k = 0; k < min(nk, kThinStages - 1); ++k) {
-      if (F > 0) {
-        prefetch_3d(m, k * kBK, nt * 64, c2);
-        prefetch_3d(m, k * kBK, F + nt * 64, c2);
-      } else {
-        prefetch_3d(m, k * kBK, nt * 128, c2);
-      }
-    }
+    const int e = __ldcg(tile_expert + b / nN), r = b % nN * ch;
+    for (int k = 0; k < min(nk, stages * kThinKb); k += kThinKb)
+      prefetch_k(e >= E ? ws : w, k, r, e >= E ? 0 : e);
   }
 };
 
@@ -489,33 +495,33 @@ struct ThinParams {
   __nv_bfloat16* o;              // I8_STORE out [rows_max, cols]
 };
 
-template <int EPI>
+template <int EPI, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
                     const __grid_constant__ CUtensorMap mapWs,
                     const __grid_constant__ CUtensorMap mapT,
                     const __grid_constant__ CUtensorMap mapN,
                     const __grid_constant__ CUtensorMap mapNs, const ThinParams tp) {
-  using S = ThinSmem;
+  using S = ThinSmem<NT>;
   const Params& p = tp.p;
-  constexpr int STAGES = thin_stages<EPI>(), NACC = S::NACC;
+  constexpr int STAGES = S::kStages, NACC = S::NACC, KB = kThinKb;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag_s;
   volatile int* abort_flag = &abort_flag_s;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t bars = base + kThinStages * S::kStage;
+  const uint32_t bars = base + S::kBarOff;
   auto full_bar = [&](int s) { return bars + 8u * s; };
-  auto empty_bar = [&](int s) { return bars + 8u * (kThinStages + s); };
-  auto accf_bar = [&](int b) { return bars + 8u * (2 * kThinStages + b); };
-  auto acce_bar = [&](int b) { return bars + 8u * (2 * kThinStages + NACC + b); };
-  const uint32_t done_bar = bars + 8u * (2 * kThinStages + 2 * NACC);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kThinStages * S::kStage + S::kBars);
-  float* swap = reinterpret_cast<float*>(gbase + (kThinStages - 1) * S::kStage);   // I8_SWIGLU
+  auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
+  auto accf_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
+  auto acce_bar = [&](int b) { return bars + 8u * (2 * STAGES + NACC + b); };
+  const uint32_t done_bar = bars + 8u * (2 * STAGES + 2 * NACC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + S::kBarOff + S::kBars);
+  float* swap = reinterpret_cast<float*>(gbase + S::kSwapOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr uint32_t kCols = NACC * kThinTok;
+  constexpr uint32_t kCols = NACC * S::kAccCols;
   if (threadIdx.x == 0) {
     abort_flag_s = 0;
     for (int s = 0; s < STAGES; ++s) {
@@ -557,9 +563,10 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
     // unused)
     return T{__ldcg(p.tile_expert + mt), mt * BM, nt * kCh, max(1, __ldcg(p.tile_rows + mt))};
   };
-  auto load_weights = [&](const CUtensorMap* mw, uint32_t sw, uint32_t fb, int k0, int n0, int ew) {
-    tma_3d(sw, mw, fb, k0, n0, ew);
-    if (EPI == I8_SWIGLU) tma_3d(sw + 64 * kBK, mw, fb, k0, p.F + n0, ew);
+  const uint64_t pol = policy_normal();
+  auto load_weights = [&](int s, int kb, int n0, int e) {
+    tma_k(base + s * S::kStage, e >= p.E ? &mapWs : &mapW, full_bar(s), kb, n0, 0,
+          e >= p.E ? 0 : e, pol);
   };
   // The first stages' weights are requested before the wait for the previous
   // kernel of the stream: they and the dispatch's tables are older than it
@@ -571,11 +578,10 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
   if (warp == 0 && lane == 0 && (int)blockIdx.x < total) {
     const int t = blockIdx.x;
     const int e = __ldcg(p.tile_expert + t / p.nN), n0 = t % p.nN * kCh;
-    early = min(STAGES, p.nk);
+    early = min(STAGES, (p.nk + KB - 1) / KB);
     for (int s = 0; s < early; ++s) {
-      mbar_expect_only(full_bar(s), S::kA);
-      load_weights(e >= p.E ? &mapWs : &mapW, base + s * S::kStage, full_bar(s), s * kBK, n0,
-                   e >= p.E ? 0 : e);
+      mbar_expect_only(full_bar(s), KB * S::kA);
+      load_weights(s, s * KB, n0, e);
     }
   }
   pdl_begin();
@@ -592,25 +598,19 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         const T d = nxt;
         nxt = decode_at(t + gridDim.x);
-        const CUtensorMap* mw = d.e >= p.E ? &mapWs : &mapW;
-        const int ew = d.e >= p.E ? 0 : d.e;
-        for (int r0 = 0; r0 < d.rows && ok; r0 += kThinTok) {
-          const int pieces = (min(kThinTok, d.rows - r0) + 15) / 16;
-          for (int kb = 0; kb < p.nk; ++kb) {
+        for (int r0 = 0; r0 < d.rows && ok; r0 += NT) {
+          for (int kb = 0; kb < p.nk; kb += KB) {
             if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
-            const uint32_t sw = base + stage * S::kStage, st = sw + S::kA;
             const uint32_t fb = full_bar(stage);
-            const int k0 = kb * kBK;
             if (early > 0) {              // weights on their way already
               --early;
-              mbar_expect_tx(fb, pieces * 16 * kBK);
+              mbar_expect_tx(fb, KB * S::kB);
             } else {
-              mbar_expect_tx(fb, S::kA + pieces * 16 * kBK);
-              load_weights(mw, sw, fb, k0, d.n0, ew);
+              mbar_expect_tx(fb, S::kStage);
+              load_weights(stage, kb, d.n0, d.e);
             }
             issued_parity[stage] = (int)phase;
-            for (int i = 0; i < pieces; ++i)
-              tma_3d(st + i * 16 * kBK, &mapT, fb, k0, d.m0 + r0 + 16 * i, 0);
+            tma_k(base + stage * S::kStage + KB * S::kA, &mapT, fb, kb, d.m0 + r0, 0, 0, pol);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
         }
@@ -623,6 +623,7 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      constexpr uint32_t idesc = idesc_i8(BM, NT);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -630,20 +631,23 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         const T d = nxt;
         nxt = decode_at(t + gridDim.x);
-        for (int r0 = 0; r0 < d.rows && ok; r0 += kThinTok) {
-          const int n = (min(kThinTok, d.rows - r0) + 15) / 16 * 16;
-          const uint32_t idesc = idesc_i8(BM, n);
+        for (int r0 = 0; r0 < d.rows && ok; r0 += NT) {
           if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t dt = tmem + acc * kThinTok;
-          for (int kb = 0; kb < p.nk; ++kb) {
+          const uint32_t dt = tmem + acc * S::kAccCols;
+          for (int kb = 0; kb < p.nk; kb += KB) {
             if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t sw = base + stage * S::kStage, st = sw + S::kA;
 #pragma unroll
-            for (int ks = 0; ks < kBK / kUmmaK; ++ks)
-              umma_i8(dt, sw128_desc(sw + ks * kUmmaK, 16, 1024),
-                      sw128_desc(st + ks * kUmmaK, 16, 1024), idesc, (kb | ks) != 0 ? 1u : 0u);
+            for (int j = 0; j < KB; ++j) {      // (a block past the last holds zeros)
+              const uint32_t sw = base + stage * S::kStage + j * S::kA;
+              const uint32_t st = base + stage * S::kStage + KB * S::kA + j * S::kB;
+#pragma unroll
+              for (int ks = 0; ks < kBK / kUmmaK; ++ks)
+                umma_i8(dt, sw128_desc(sw + ks * kUmmaK, 16, 1024),
+                        sw128_desc(st + ks * kUmmaK, 16, 1024), idesc,
+                        (kb | j | ks) != 0 ? 1u : 0u);
+            }
             umma_commit(empty_bar(stage));
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
@@ -670,9 +674,10 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
       // this lane's channel: of the outputs, or of F with its gate or up scale
       const int ch = EPI == I8_SWIGLU ? d.n0 + (q & 1) * 32 + lane : d.n0 + q * 32 + lane;
       const float ws = cs[EPI == I8_SWIGLU && q >= 2 ? p.F + ch : ch];
-      for (int r0 = 0; r0 < d.rows; r0 += kThinTok) {
+      for (int r0 = 0; r0 < d.rows; r0 += NT) {
         const int row0 = d.m0 + r0 + hh * 32;
-        const int cnt = min(32, d.rows - r0 - hh * 32);   // tokens of this warp (may be <= 0)
+        // tokens of this warp (may be <= 0; with one half, none of hh = 1)
+        const int cnt = hh < S::kHalves ? min(min(32, NT), d.rows - r0 - hh * 32) : 0;
         float rs = 0.f;                                   // lane j: scale of token j
         if (lane < cnt)
           rs = EPI == I8_SWIGLU ? p.row_scale[row0 + lane] : scale_of(p.row_max[row0 + lane]);
@@ -685,7 +690,7 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
         tc_fence_after();
         uint32_t r[32];
         if (cnt > 0) {
-          tmem_ld32(tmem + acc * kThinTok + hh * 32 + ((uint32_t)(q * 32) << 16), r);
+          tmem_ld32(tmem + acc * S::kAccCols + hh * 32 + ((uint32_t)(q * 32) << 16), r);
           tmem_wait();
         }
         tc_fence_before();

@@ -19,10 +19,13 @@ int after_launch(cudaStream_t s, const char* name);    // counts, checks, timing
 bool use_pdl();
 int sm_count();                                        // of the current device
 
-// cuTensorMapEncodeTiled for one- to three-dimensional tensors of 1-byte
-// elements [n3][rows][cols], 128-byte swizzle, box {128, box_rows, 1}.
-int make_map_u8(CUtensorMap* m, const void* ptr, int64_t n3, int64_t rows, int64_t cols,
-                uint32_t box_rows);
+// 8-bit matrices [n][halves][rows][K] for loads of several 128-byte k blocks
+// at once: seen as [n][K / 128][halves][rows][128], 128-byte swizzle, box
+// {128, box_rows, box_halves, kb, 1}, which lands in shared memory k block by
+// k block, each as its rows of 128 swizzled bytes.  k blocks past K / 128
+// read zeros.
+int make_map_k(CUtensorMap* m, const void* ptr, int64_t n, int64_t halves, int64_t rows, int64_t K,
+               uint32_t box_rows, uint32_t box_halves, uint32_t kb);
 // TMA-store targets [rows][cols]: bf16 (64-byte swizzle) or fp32 (128-byte
 // swizzle), 32 x 32 boxes.
 int make_out_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, bool fp32);

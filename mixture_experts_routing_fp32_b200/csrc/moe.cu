@@ -2193,15 +2193,17 @@ int sm_count() {
   return known[dev];
 }
 
-int make_map_u8(CUtensorMap* m, const void* ptr, int64_t n3, int64_t rows, int64_t cols,
-                uint32_t box_rows) {
+int make_map_k(CUtensorMap* m, const void* ptr, int64_t n, int64_t halves, int64_t rows, int64_t K,
+               uint32_t box_rows, uint32_t box_halves, uint32_t kb) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return fail(cudaErrorNotSupported);
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n3};
-  cuuint64_t strides[2] = {(cuuint64_t)cols, (cuuint64_t)(rows * cols)};
-  cuuint32_t box[3] = {128, box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides,
+  cuuint64_t dims[5] = {128, (cuuint64_t)rows, (cuuint64_t)halves, (cuuint64_t)(K / 128),
+                        (cuuint64_t)n};
+  cuuint64_t strides[4] = {(cuuint64_t)K, (cuuint64_t)(rows * K), 128,
+                           (cuuint64_t)(halves * rows * K)};
+  cuuint32_t box[5] = {128, box_rows, box_halves, kb, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(ptr), dims, strides,
                         box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MOE_OK : fail(cudaErrorInvalidValue);

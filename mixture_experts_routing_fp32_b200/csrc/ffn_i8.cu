@@ -278,9 +278,15 @@ int group_rows(int64_t k_bytes, bool pair) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(64, (24ll << 20) / (rows * k_bytes)));
 }
 
-// Few rows per expert: the weights' way in bounds the product.
+// Few rows per expert: the weights' way in bounds the product.  A layer pass,
+// thin against general kernels: at 8 and 16 rows per expert 101 against 105
+// and 106 against 111 us (OLMoE-shaped), at 16 rows 255 against 262
+// (Mixtral-shaped), at 24 rows 116 against 113 and 259 against 266, at 64 rows
+// 168 against 129.  The shared expert's T rows run in turns over its weights:
+// at 64 tokens the thin form already loses (37 against 33 us, 32 experts of
+// 1024 x 512).
 bool few_rows(const moe_config_t* c, const Work& w) {
-  return (int64_t)c->T * c->K <= 32ll * w.v.local_experts;
+  return (int64_t)c->T * c->K <= 16ll * w.v.local_experts && (c->n_shared == 0 || c->T <= 32);
 }
 
 // Maps and shape of one thin product's weights.

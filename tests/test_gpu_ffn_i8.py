@@ -177,6 +177,11 @@ CASES = [
     dict(T=1, D=128, E=4, K=1, F=128), dict(T=1, D=256, E=64, K=8, F=128, shared=True),
     dict(T=3, D=384, E=8, K=2, F=640), dict(T=16, D=512, E=8, K=2, F=1792),
     dict(T=37, D=128, E=5, K=3, F=384, shared=True, holes=0.3),
+    # few rows per expert: 16, 32 and 64 columns of tokens, turns (one expert
+    # picked by all 150 tokens), an odd number of k blocks, the shared expert
+    dict(T=7, D=384, E=16, K=2, F=128, shared=True), dict(T=29, D=640, E=16, K=4, F=384, shared=True),
+    dict(T=60, D=256, E=32, K=4, F=640, holes=0.2), dict(T=150, D=384, E=64, K=2, F=256, hot=9.0),
+    dict(T=32, D=128, E=64, K=8, F=128, hot=9.0, capacity_factor=2.0),
     dict(T=130, D=256, E=4, K=4, F=256, hot=3.0),                 # select all
     dict(T=333, D=1024, E=32, K=4, F=512, shared=True, holes=0.1),
     dict(T=400, D=256, E=16, K=6, F=128, capacity_factor=0.7),    # drops

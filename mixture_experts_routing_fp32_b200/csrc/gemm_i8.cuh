@@ -16,6 +16,7 @@
 // bounds it sooner.  Experts of few rows (decoding) run in a second
 // kernel, at the end of this file.
 #pragma once
+#include "f32x2.cuh"
 #include "gemm_tc.cuh"
 
 namespace moe {
@@ -353,26 +354,44 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
           }
           if (valid) atomicMax(p.row_max + row0 + lane, big);
         } else {
-          constexpr int HC = BN / 2;
-#pragma unroll 1
-          for (int c = 0; c < HC; c += 32) {
-            uint32_t r[32];
-            tmem_ld32(trow + hh * HC + c, r);
-            const int n = d.n0 + hh * HC + c;
-            const float4* cn = reinterpret_cast<const float4*>(cs + n);
-            tmem_wait();
-            float v[32];
+          // 32 columns at a time; the next ones' accumulators and scales are
+          // on their way while these are scaled and stored (a chunk that
+          // waits for its own took 1400 cycles, four of them longer than a
+          // short tile's products)
+          constexpr int NC = BN / 2 / 32;
+          const int n = d.n0 + hh * (BN / 2);
+          const uint32_t at = trow + hh * (BN / 2);
+          const float4* cn = reinterpret_cast<const float4*>(cs + n);
+          uint32_t r[2][32];
+          float4 sc[2][8];
+          tmem_ld32(at, r[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 s = __ldg(cn + i);
-              v[4 * i] = __int2float_rn((int)r[4 * i]) * (rs * s.x);
-              v[4 * i + 1] = __int2float_rn((int)r[4 * i + 1]) * (rs * s.y);
-              v[4 * i + 2] = __int2float_rn((int)r[4 * i + 2]) * (rs * s.z);
-              v[4 * i + 3] = __int2float_rn((int)r[4 * i + 3]) * (rs * s.w);
+          for (int i = 0; i < 8; ++i) sc[0][i] = __ldg(cn + i);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            tmem_wait();
+            if (c + 1 < NC) {
+              tmem_ld32(at + 32 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sc[(c + 1) & 1][i] = __ldg(cn + 8 * (c + 1) + i);
             }
+            const uint32_t(&a)[32] = r[c & 1];
+            const uint64_t rs2 = pack2(rs, rs);
             uint4 u[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = pack8_bf16(v + 8 * j);
+            for (int j = 0; j < 4; ++j) {
+              F8 v;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float4 w = sc[c & 1][2 * j + i];
+                const uint32_t* q4 = a + 8 * j + 4 * i;
+                v.p[2 * i] = mul2(pack2(__int2float_rn((int)q4[0]), __int2float_rn((int)q4[1])),
+                                  mul2(rs2, pack2(w.x, w.y)));
+                v.p[2 * i + 1] = mul2(pack2(__int2float_rn((int)q4[2]), __int2float_rn((int)q4[3])),
+                                      mul2(rs2, pack2(w.z, w.w)));
+              }
+              u[j] = narrow8(v);
+            }
             const uint32_t buf = stg + box * kTmaBox;
             box ^= 1;
             if (lane == 0) bulk_wait_read_1();
@@ -381,7 +400,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&mapO, buf, n, row0);
+              tma_store_2d(&mapO, buf, n + 32 * c, row0);
               bulk_commit();
             }
           }

@@ -504,7 +504,7 @@ enum { MOE_RMSNORM = 0, MOE_LAYERNORM = 1 };     /* moe_norm_config_t.norm */
  *   gate_len  tokens that share a row of `gate`: token t takes row
  *           t / gate_len of [ceil(T / gate_len), D] (a sequence's gate, or
  *           with gate_len = T one gate for all); 0: no gate
- * Limits: T >= 1, 8 <= D <= 8192, D % 8 == 0; eps > 0.  Sums and
+ * Limits: 1 <= T <= 2^30, 8 <= D <= 8192, D % 8 == 0; eps > 0.  Sums and
  * statistics are fp32.
  */
 typedef struct {

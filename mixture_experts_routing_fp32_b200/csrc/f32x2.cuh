@@ -92,6 +92,11 @@ __device__ __forceinline__ void store_f8(float* p, const F8& a) {
   *reinterpret_cast<float4*>(p) = make_float4(q0.x, q0.y, q1.x, q1.y);
   *reinterpret_cast<float4*>(p + 4) = make_float4(q2.x, q2.y, q3.x, q3.y);
 }
+__device__ __forceinline__ void store_f8_split(float4* lo, float4* hi, const F8& a) {
+  const float2 q0 = unpack2(a.p[0]), q1 = unpack2(a.p[1]), q2 = unpack2(a.p[2]), q3 = unpack2(a.p[3]);
+  *lo = make_float4(q0.x, q0.y, q1.x, q1.y);
+  *hi = make_float4(q2.x, q2.y, q3.x, q3.y);
+}
 __device__ __forceinline__ uint4 narrow8(const F8& a) {
   uint4 u;
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);

@@ -47,6 +47,8 @@ struct NormArgs {
   float* dgate;
   float* part;                       // partial column sums, kSlots arrays of [P][D]
   int several;                       // gate rows change inside the batch
+  int bias_smem;                     // forward: the biases sit in shared memory too
+  int w_smem;                        // backward: the running sums for w_post do
 };
 
 // Partial column sums a CTA leaves (arrays of [P][D] floats in this order).
@@ -81,7 +83,26 @@ __device__ __forceinline__ void fetch(uint32_t slot, int pitch, const T* p) {
   if constexpr (sizeof(T) == 4) cp16(slot + pitch, p + 4);
 }
 // This thread's piece back from its slot (bf16 rows use one 16-byte chunk,
-// fp32 rows two).
+// fp32 rows two), and a piece of its own put there.  The backward, short of
+// registers, addresses its slots in 32 bits (16384 rows of 4096 bf16: 142 us
+// against 172); the forward is the faster with plain loads, which the
+// compiler moves (91 us against 102).
+__device__ __forceinline__ float4 lds(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ F8 take(uint32_t slot, int pitch) {
+  const float4 a = lds(slot);
+  if constexpr (sizeof(T) == 2)
+    return widen8(make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z),
+                             __float_as_uint(a.w)));
+  else return f8_of(a, lds(slot + pitch));
+}
 template <typename T>
 __device__ __forceinline__ F8 take(const uint8_t* slot, int pitch) {
   if constexpr (sizeof(T) == 2) return widen8(*reinterpret_cast<const uint4*>(slot));
@@ -89,33 +110,54 @@ __device__ __forceinline__ F8 take(const uint8_t* slot, int pitch) {
                     *reinterpret_cast<const float4*>(slot + pitch));
 }
 __device__ __forceinline__ void keep(uint8_t* slot, int pitch, const F8& a) {
-  const float2 q0 = unpack2(a.p[0]), q1 = unpack2(a.p[1]), q2 = unpack2(a.p[2]), q3 = unpack2(a.p[3]);
-  *reinterpret_cast<float4*>(slot) = make_float4(q0.x, q0.y, q1.x, q1.y);
-  *reinterpret_cast<float4*>(slot + pitch) = make_float4(q2.x, q2.y, q3.x, q3.y);
+  store_f8_split(reinterpret_cast<float4*>(slot), reinterpret_cast<float4*>(slot + pitch), a);
+}
+__device__ __forceinline__ void keep(uint32_t slot, int pitch, const F8& a) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 p = unpack2(a.p[2 * i]), q = unpack2(a.p[2 * i + 1]);
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(slot + i * pitch), "f"(p.x),
+                 "f"(p.y), "f"(q.x), "f"(q.y)
+                 : "memory");
+  }
 }
 
-// Sums of a and b over the tpr threads of a row group (all get them, in the
-// same order).  `buf` alternates, so one barrier per sum is enough: a warp
-// still reading one buffer is behind the barrier of the next sum, which
-// writes the other.
+// Sums over the tpr threads of a row group (all get them, in the same order).
+// `buf` alternates, so one barrier per sum is enough: a warp still reading
+// one buffer is behind the barrier of the next sum, which writes the other.
 struct RowSum {
   float2* red;      // [2][32] of this row group
   int warps, warp, lane, bar, tpr, buf;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (warps == 1) return make_float2(a, b);
-    if (lane == 0) red[buf * 32 + warp] = make_float2(a, b);
+  __device__ __forceinline__ void sync() const {
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
-    const float2 v = lane < warps ? red[buf * 32 + lane] : make_float2(0.f, 0.f);
+  }
+  // Two values in the shuffles of one: the halves of the warp exchange what
+  // the other half goes on to sum.  a's sum is left in lanes 0-15, b's in
+  // 16-31.
+  __device__ __forceinline__ float halves(float a, float b) const {
+    const bool hi = (lane & 16) != 0;
+    float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ __forceinline__ float2 spread(float v) const {
+    return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+  }
+  __device__ __forceinline__ float2 operator()(float a, float b) {
+    float v = halves(a, b);
+    if (warps == 1) return spread(v);
+    if ((lane & 15) == 0) reinterpret_cast<float*>(red + buf * 32 + warp)[lane >> 4] = v;
+    sync();
+    const float2 w = lane < warps ? red[buf * 32 + lane] : make_float2(0.f, 0.f);
     buf ^= 1;
-    return make_float2(warp_sum(v.x), warp_sum(v.y));
+    return spread(halves(w.x, w.y));
   }
   __device__ __forceinline__ float operator()(float a) {
     a = warp_sum(a);
     if (warps == 1) return a;
-    if (lane == 0) red[buf * 32 + warp] = make_float2(a, 0.f);
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+    if (lane == 0) red[buf * 32 + warp].x = a;
+    sync();
     const float v = lane < warps ? red[buf * 32 + lane].x : 0.f;
     buf ^= 1;
     return warp_sum(v);
@@ -129,7 +171,9 @@ __device__ __forceinline__ int first_row(int T, int p, int P) {
 
 // mean and rstd of a row held 8 values a thread (zeros in idle threads).
 // The variance is that of the centred values (a second sum), so a mean that
-// is large against the spread costs no digits.
+// is large against the spread costs no digits.  (Joining each warp's own
+// centred sums instead, with one exchange, measured 166 against 142 us for
+// 16384 rows of 4096 bf16: its chain of shuffles is as long.)
 __device__ __forceinline__ float2 moments(const F8& v, bool active, const NormArgs& a,
                                           RowSum& sum) {
   if (!a.layer) return make_float2(0.f, rsqrtf(fmaf(sum(dot8(v, v)), a.inv_d, a.eps)));
@@ -185,7 +229,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
   };
   for (int i = 0; i < a.stages - 1; ++i) issue();
   if (a.w_pre != nullptr) keep(v_pre, pitch, active ? load_f8(a.w_pre + c0) : zero8f());
-  if (BIAS && a.w_pre != nullptr)
+  if (BIAS && a.bias_smem && a.w_pre != nullptr)
     keep(v_bpre, pitch, active && a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
   // alpha gate w_post and alpha gate b_post of gate row gr
   auto post_vectors = [&](int gr) {
@@ -196,7 +240,13 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
       if (a.w_post != nullptr) e = mul8(e, load_f8(a.w_post + c0));
     }
     keep(v_post, pitch, e);
-    if (BIAS) keep(v_bpost, pitch, eb);
+    if (BIAS && a.bias_smem) keep(v_bpost, pitch, eb);
+  };
+  // alpha gate b_post and b_pre where the ring leaves no room for them
+  auto post_bias = [&](int gr) {
+    if (!active || a.b_post == nullptr) return zero8f();
+    F8 eb = mul8(load_f8(a.b_post + c0), pack2(a.alpha, a.alpha));
+    return a.gate_len > 0 ? mul8(eb, load_f8(a.gate + (int64_t)gr * a.D + c0)) : eb;
   };
   int gate_row = -1;
   const uint8_t* slot = mine;
@@ -219,7 +269,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
         const float c = -my.x * my.y;
         z = fma8(z, pack2(my.y, my.y), pack2(c, c));
       }
-      if (BIAS) v = add8(v, take<float>(v_bpost, pitch));
+      if (BIAS) v = add8(v, a.bias_smem ? take<float>(v_bpost, pitch) : post_bias(gate_row));
       v = fma8(z, take<float>(v_post, pitch), v);
       TR* out = static_cast<TR*>(a.r_out) + at;
       // the second norm reads the stream as it is stored: the backward then
@@ -237,7 +287,10 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
       mr = moments(v, active, a, sum);
       const float c = -mr.x * mr.y;
       v = fma8(v, pack2(mr.y, mr.y), pack2(c, c));
-      if (BIAS) v = fma8(v, take<float>(v_pre, pitch), take<float>(v_bpre, pitch));
+      if (BIAS)
+        v = fma8(v, take<float>(v_pre, pitch),
+                 a.bias_smem ? take<float>(v_bpre, pitch)
+                 : active && a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
       else v = mul8(v, take<float>(v_pre, pitch));
       if (active) store_f8(static_cast<TA*>(a.x) + at, v);
     }
@@ -283,15 +336,14 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   constexpr int kA = kPiece<TA> / 16, kR = kPiece<TR> / 16, kW = GENERAL ? 2 : 1;
   const int stage_bytes = 2 * (kA + kR) * pitch;
   const int o_dx = kA * pitch, o_r = 2 * kA * pitch, o_g = (2 * kA + kR) * pitch;
-  uint8_t* mine = ring + tid * 16;
-  const uint32_t mine_a = smem_addr(mine);
+  const uint32_t mine = smem_addr(ring) + tid * 16;
   // after the ring: this thread's 8 columns of w_pre and of alpha gate w_post,
-  // [kW][D] running sums for w_post, b_post (SEVERAL), and one [R][8 tpr]
-  // exchange buffer (R > 1)
-  uint8_t* v_pre = mine + a.stages * stage_bytes;
-  uint8_t* v_post = v_pre + 2 * pitch;
-  float* w_sum = reinterpret_cast<float*>(ring + a.stages * stage_bytes + 4 * pitch);
-  float* swap = w_sum + (SEVERAL ? kW * a.D : 0);
+  // [kW][D] running sums for w_post, b_post (SEVERAL, where they fit; else
+  // the CTA's partial in global memory), and one [R][8 tpr] exchange buffer
+  // (R > 1)
+  const uint32_t v_pre = mine + a.stages * stage_bytes, v_post = v_pre + 2 * pitch;
+  float* w_smem = reinterpret_cast<float*>(ring + a.stages * stage_bytes + 4 * pitch);
+  float* swap = w_smem + (SEVERAL && a.w_smem ? kW * a.D : 0);
   const TA* y = static_cast<const TA*>(a.y);
   const TA* dx = static_cast<const TA*>(a.dx);
   const TR* r = static_cast<const TR*>(a.r);
@@ -301,33 +353,22 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   const int64_t arr = (int64_t)P * a.D;             // floats of one partial array
   float* part = a.part + (int64_t)p * a.D + c0;
 
-  if (SEVERAL && active && g == 0) {
-    for (int k = 0; k < kW; ++k) store_f8(w_sum + k * a.D + c0, zero8f());
-  }
   pdl_begin();
+  float* w_sum[2] = {a.w_smem ? w_smem + c0 : part + W1 * arr,
+                     a.w_smem ? w_smem + a.D + c0 : part + W2 * arr};
+  if (SEVERAL && active && g == 0) {
+    for (int k = 0; k < kW; ++k) store_f8(w_sum[k], zero8f());
+  }
 
-  // rows of a segment: [seg0, seg1), row group g takes seg0 + g, + R, ...
+  // Row group g takes rows row0 + g, + R, ...; segments are runs of rows of
+  // one gate row, at whose ends the groups meet.
   const int L = SEVERAL ? a.gate_len : a.T;
   auto seg_end = [&](int row) {
     return SEVERAL ? (int)min((int64_t)row1, (int64_t)(row / L + 1) * L) : row1;
   };
-  // this row group's first row in the segments from s0 on (row1: none)
-  auto first_in = [&](int s0) {
-    while (s0 < row1) {
-      const int e = seg_end(s0);
-      if (s0 + g < e) return s0 + g;
-      s0 = e;
-    }
-    return row1;
-  };
-  auto next_row = [&](int t) {
-    if constexpr (!SEVERAL) return min(t + a.R, row1);
-    const int e = seg_end(t);
-    return t + a.R < e ? t + a.R : first_in(e);
-  };
-  int ahead = first_in(row0);
-  uint32_t slot_in = mine_a;
-  const uint32_t ring_end = mine_a + a.stages * stage_bytes;
+  int ahead = row0 + g;
+  uint32_t slot_in = mine;
+  const uint32_t ring_end = mine + a.stages * stage_bytes;
   auto issue = [&] {
     if (a.stages == 0) return;
     if (ahead < row1) {
@@ -340,11 +381,11 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
         }
         if (gin != nullptr) fetch<TR>(slot_in + o_g, pitch, gin + at);
       }
-      ahead = next_row(ahead);
+      ahead += a.R;
     }
     cp_commit();
     slot_in += stage_bytes;
-    if (slot_in == ring_end) slot_in = mine_a;
+    if (slot_in == ring_end) slot_in = mine;
   };
   F8 s1 = zero8f(), p1 = zero8f(), s2 = zero8f(), p2 = zero8f();
   // sum of v over the row groups, in group order (in group 0's threads)
@@ -359,12 +400,13 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
 
   const float4* stats = reinterpret_cast<const float4*>(a.stats_in);
   float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ahead < row1) st_next = stats[ahead];
+  int t = row0 + g;
+  if (t < row1) st_next = stats[t];
   for (int i = 0; i < a.stages - 1; ++i) issue();
   // idle threads of a row's last warp hold zeros in both vectors and in
   // every tensor they weight, so they add nothing to the row's sums
   keep(v_pre, pitch, active && a.w_pre != nullptr ? load_f8(a.w_pre + c0) : zero8f());
-  const uint8_t* slot = mine;
+  uint32_t slot = mine;
   for (int seg0 = row0; seg0 < row1;) {
     const int seg1 = seg_end(seg0);
     const float* gate = a.gate_len > 0 ? a.gate + (int64_t)(seg0 / a.gate_len) * a.D + c0 : nullptr;
@@ -377,11 +419,10 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
       }
       keep(v_post, pitch, w);
     }
-    for (int t = seg0 + g; t < seg1; t += a.R) {
+    for (; t < seg1; t += a.R) {
       issue();
       const float4 st = st_next;
-      const int tn = next_row(t);
-      if (tn < row1) st_next = stats[tn];
+      if (t + a.R < row1) st_next = stats[t + a.R];
       const int64_t at = (int64_t)t * a.D + c0;
       if (a.stages > 0) cp_wait(a.stages - 1);
       // this thread's columns of one tensor (rows that fit no ring: from
@@ -437,15 +478,15 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
         if (active) store_f8(static_cast<TA*>(a.dy) + at, e);
       }
       slot += stage_bytes;
-      if (smem_addr(slot) == ring_end) slot = mine;
+      if (slot == ring_end) slot = mine;
     }
     if constexpr (SEVERAL) {
       join(s1);
       if (GENERAL) join(s2);
       if (g == 0 && active) {
         const F8 wg = load_f8(gate);
-        store_f8(w_sum + c0, fma8(wg, s1, load_f8(w_sum + c0)));
-        if (GENERAL) store_f8(w_sum + a.D + c0, fma8(wg, s2, load_f8(w_sum + a.D + c0)));
+        store_f8(w_sum[0], fma8(wg, s1, load_f8(w_sum[0])));
+        if (GENERAL) store_f8(w_sum[1], fma8(wg, s2, load_f8(w_sum[1])));
         const int gr = seg0 / L;
         const int64_t gs = (int64_t)gr * L, ge = min((int64_t)a.T, gs + L);
         if (gs >= row0 && ge <= row1) {
@@ -482,9 +523,9 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
       if (g == 0 && active) store_f8(part + P2 * arr, p2);
     }
   }
-  if (SEVERAL && g == 0 && active) {
-    store_f8(part + W1 * arr, load_f8(w_sum + c0));
-    if (GENERAL) store_f8(part + W2 * arr, load_f8(w_sum + a.D + c0));
+  if (SEVERAL && a.w_smem && g == 0 && active) {
+    store_f8(part + W1 * arr, load_f8(w_sum[0]));
+    if (GENERAL) store_f8(part + W2 * arr, load_f8(w_sum[1]));
   }
 }
 
@@ -500,61 +541,68 @@ struct SumArgs {
 };
 
 __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const SumArgs s) {
-  __shared__ float tile[32][33];
+  __shared__ float tile[4][32][33];
   const NormArgs& a = s.n;
   const int cx = threadIdx.x & 31, strand = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + cx;
   const bool in = col < a.D;
   const int64_t arr = (int64_t)s.P * a.D;
   pdl_begin();
-  // over CTAs [p0, p1) of array `which` (the same in every thread of a column)
-  auto add = [&](int which, int p0, int p1) {
-    const float* at = a.part + which * arr + col;
-    float v = 0.f;
+  // Sums over CTAs [p0, p1) of up to four arrays (which[i] < 0: none), all
+  // loads before the first exchange; the sums of column cx end in every
+  // thread of it.
+  auto add = [&](const int (&which)[4], int p0, int p1, float (&out)[4]) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (in) {
-#pragma unroll 4
-      for (int p = p0 + strand; p < p1; p += 32) v += at[(int64_t)p * a.D];
+#pragma unroll 2
+      for (int p = p0 + strand; p < p1; p += 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (which[i] >= 0) v[i] += a.part[which[i] * arr + (int64_t)p * a.D + col];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tile[i][strand][cx] = v[i];
+    __syncthreads();
+    // the warp's lanes take the 32 strands of column `strand`
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = which[i] >= 0 ? warp_sum(tile[i][cx][strand]) : 0.f;
+    __syncthreads();
+    if (cx == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tile[i][0][strand] = v[i];
     }
     __syncthreads();
-    tile[strand][cx] = v;
-    __syncthreads();
-    float t = tile[cx][strand];     // the warp's 32 strands of column `strand`
-    t = warp_sum(t);
-    __syncthreads();
-    if (cx == 0) tile[0][strand] = t;
-    __syncthreads();
-    return tile[0][cx];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = tile[i][0][cx];
   };
-  auto gate_grad = [&](float s1, float s2) {
-    float o = a.w_post != nullptr ? a.w_post[col] * s1 : s1;
-    if (a.b_post != nullptr) o = fmaf(a.b_post[col], s2, o);
+  auto gate_grad = [&](float s1, float s2, int c) {
+    float o = a.w_post != nullptr ? a.w_post[c] * s1 : s1;
+    if (a.b_post != nullptr) o = fmaf(a.b_post[c], s2, o);
     return a.alpha * o;
   };
   if (blockIdx.y == 0) {
-    const bool bias_y = s.db_post != nullptr || (a.dgate != nullptr && a.b_post != nullptr);
-    if (a.y != nullptr && (s.dw_post != nullptr || s.db_post != nullptr || !a.several)) {
-      const float s1 = add(a.several ? W1 : S1H, 0, s.P);
-      const float s2 = bias_y ? add(a.several ? W2 : S2H, 0, s.P) : 0.f;
-      if (in && strand == 0) {
-        // several gate rows: the sums already hold the gate
-        const float gate = (a.gate_len > 0 && !a.several) ? a.gate[col] : 1.f;
-        if (s.dw_post != nullptr) s.dw_post[col] = a.alpha * gate * s1;
-        if (s.db_post != nullptr) s.db_post[col] = a.alpha * gate * s2;
-        if (a.dgate != nullptr && !a.several) a.dgate[col] = gate_grad(s1, s2);
-      }
-    }
-    if (s.dw_pre != nullptr) {
-      const float v = add(P1, 0, s.P);
-      if (in && strand == 0) s.dw_pre[col] = v;
-    }
-    if (s.db_pre != nullptr) {
-      const float b = add(P2, 0, s.P);
-      if (in && strand == 0) s.db_pre[col] = b;
-    }
+    float v[4];
+    const bool gate1 = a.dgate != nullptr && !a.several;
+    const bool s1 = a.y != nullptr && (s.dw_post != nullptr || gate1);
+    const bool s2 = a.y != nullptr && (s.db_post != nullptr || (gate1 && a.b_post != nullptr));
+    // several gate rows: the sums already hold the gate
+    const int which[4] = {s1 ? (a.several ? W1 : S1H) : -1, s2 ? (a.several ? W2 : S2H) : -1,
+                          s.dw_pre != nullptr ? P1 : -1, s.db_pre != nullptr ? P2 : -1};
+    add(which, 0, s.P, v);
+    if (!in || strand != 0) return;
+    const float gate = (a.gate_len > 0 && !a.several) ? a.gate[col] : 1.f;
+    if (s.dw_post != nullptr) s.dw_post[col] = a.alpha * gate * v[0];
+    if (s.db_post != nullptr) s.db_post[col] = a.alpha * gate * v[1];
+    if (gate1) a.dgate[col] = gate_grad(v[0], v[1], col);
+    if (s.dw_pre != nullptr) s.dw_pre[col] = v[2];
+    if (s.db_pre != nullptr) s.db_pre[col] = v[3];
     return;
   }
   // The CTA that starts the gate row left its share as its tail, those that
-  // go on with it as their heads.
+  // go on with it as their heads.  A thread takes a column (few CTAs hold a
+  // gate row), a block 1024 of them.
+  if (blockIdx.x * 1024 >= a.D) return;
   int64_t gs;
   if (s.by_row) {
     gs = (int64_t)(blockIdx.y - 1) * a.gate_len;
@@ -567,14 +615,17 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const SumArgs s) {
   auto holder = [&](int64_t row) { return (int)(((row + 1) * s.P - 1) / a.T); };
   const int pa = holder(gs), pb = holder(ge - 1);
   if (pa == pb) return;                        // whole in one CTA: written there
-  // (a row that ends where its last CTA does is cut all the same)
-  float s1 = add(S1H, pa + 1, pb + 1);
-  float s2 = a.b_post != nullptr ? add(S2H, pa + 1, pb + 1) : 0.f;
-  if (!in || strand != 0) return;
-  const float* at = a.part + (int64_t)pa * a.D + col;
-  s1 += at[S1T * arr];
-  if (a.b_post != nullptr) s2 += at[S2T * arr];
-  a.dgate[gs / a.gate_len * a.D + col] = gate_grad(s1, s2);
+  const int gc = blockIdx.x * 1024 + threadIdx.x;
+  if (gc >= a.D) return;
+  const float* at = a.part + gc;
+  float s1 = at[S1T * arr + (int64_t)pa * a.D];
+  float s2 = a.b_post != nullptr ? at[S2T * arr + (int64_t)pa * a.D] : 0.f;
+#pragma unroll 4
+  for (int p = pa + 1; p <= pb; ++p) {
+    s1 += at[S1H * arr + (int64_t)p * a.D];
+    if (a.b_post != nullptr) s2 += at[S2H * arr + (int64_t)p * a.D];
+  }
+  a.dgate[gs / a.gate_len * a.D + gc] = gate_grad(s1, s2, gc);
 }
 
 // ---------------------------------------------------------------------------
@@ -582,7 +633,7 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const SumArgs s) {
 // ---------------------------------------------------------------------------
 int check(const moe_norm_config_t* c) {
   if (c == nullptr) return MOE_ERR_ARG;
-  if (c->T < 1 || c->D < 8 || c->D > kMaxD || (c->D % 8)) return MOE_ERR_ARG;
+  if (c->T < 1 || c->T > (1 << 30) || c->D < 8 || c->D > kMaxD || (c->D % 8)) return MOE_ERR_ARG;
   if (c->norm != MOE_RMSNORM && c->norm != MOE_LAYERNORM) return MOE_ERR_ARG;
   if (c->dtype != MOE_FP32 && c->dtype != MOE_BF16) return MOE_ERR_ARG;
   if (c->resid != MOE_FP32 && c->resid != MOE_BF16) return MOE_ERR_ARG;
@@ -640,10 +691,15 @@ int forward(NormArgs a, cudaStream_t s) {
   const int threads = a.R * a.tpr;
   const bool bias = a.b_post != nullptr || a.b_pre != nullptr;
   const size_t stage = (size_t)(kPiece<TA> + kPiece<TR>) * threads;
-  const size_t fixed = (size_t)threads * 32 * (bias ? 4 : 2);
+  size_t fixed = (size_t)threads * 32 * (bias ? 4 : 2);
   // 64 registers a thread: 1024 threads of an SM
   const int per_sm = std::max(1, 1024 / threads);
   const size_t room = (kSmemLimit + 1024) / per_sm - 9 * 1024;
+  // biases in shared memory only where they leave two rows' room (16384 rows
+  // of 4096 bf16: 142 us with two rows and the biases, 172 with four rows and
+  // the biases read from L2)
+  a.bias_smem = bias && fixed + 2 * stage <= room;
+  if (!a.bias_smem) fixed = (size_t)threads * 64;
   a.stages = (int)std::max<size_t>(1, std::min<size_t>(4, (room - std::min(room, fixed)) / stage));
   const size_t smem = a.stages * stage + fixed;
   const int grid = (int)std::min<int64_t>(host::ceil_div(a.T, a.R), (int64_t)sms * per_sm);
@@ -659,14 +715,17 @@ int backward(NormArgs a, int P, bool bias, SumArgs& sum, cudaStream_t s) {
   const int threads = a.R * a.tpr;
   const bool general = bias || a.layer;
   const size_t stage = 2 * (size_t)(kPiece<TA> + kPiece<TR>) * threads;
-  const size_t fixed = (size_t)threads * 64 + (a.several ? (general ? 2 : 1) * (size_t)a.D * 4 : 0) +
-                       (a.R > 1 ? (size_t)threads * 32 : 0);
+  size_t fixed = (size_t)threads * 64 + (a.R > 1 ? (size_t)threads * 32 : 0);
   // two CTAs an SM share its shared memory (8 KB static and 1 KB of the
   // system's each)
-  const size_t room = (threads > 512 ? kSmemLimit + 1024 : (kSmemLimit + 1024) / 2) - 9 * 1024 - fixed;
+  const size_t room = (threads > 512 ? kSmemLimit + 1024 : (kSmemLimit + 1024) / 2) - 9 * 1024;
+  // the running sums for w_post where a ring of two rows still fits
+  const size_t w_bytes = (general ? 2 : 1) * (size_t)a.D * 4;
+  a.w_smem = a.several && fixed + w_bytes + 2 * stage <= room;
+  if (a.w_smem) fixed += w_bytes;
   // a ring of one stage would overlap nothing: rows too long for two (wide
   // fp32 rows) are read where they are used
-  a.stages = (int)std::min<size_t>(3, room / stage);
+  a.stages = (int)std::min<size_t>(3, (room - fixed) / stage);
   if (a.stages < 2) a.stages = 0;
   const size_t smem = a.stages * stage + fixed;
   auto go = [&](auto k) {

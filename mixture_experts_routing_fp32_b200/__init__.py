@@ -15,6 +15,7 @@ from .api import (MoEError, MoeConfig, MoeSizes, config_from, make_config,
                   moe_block_norm_backward, moe_block_norm_ws_bytes, AdamwConfig, AdamwTable,
                   adamw_table, make_adamw_config, moe_adamw, moe_expert_ffn_i8,
                   moe_expert_ffn_i8_ws_bytes, moe_quant_i8)
+from .block import MoEBlock
 from .layer_i8 import MoEInt8Layer
 from .optim import MoEAdamW
 from .layer import MoELayer
@@ -28,4 +29,4 @@ __all__ = ["MoEError", "MoeConfig", "MoeSizes", "config_from", "make_config",
            "moe_set_backward_streams", "NormConfig", "make_norm_config", "moe_block_norm",
            "moe_block_norm_backward", "moe_block_norm_ws_bytes", "AdamwConfig", "AdamwTable",
            "adamw_table", "make_adamw_config", "moe_adamw", "MoEAdamW", "moe_expert_ffn_i8",
-           "moe_expert_ffn_i8_ws_bytes", "moe_quant_i8", "MoEInt8Layer", "MoELayer"]
+           "moe_expert_ffn_i8_ws_bytes", "moe_quant_i8", "MoEInt8Layer", "MoEBlock", "MoELayer"]

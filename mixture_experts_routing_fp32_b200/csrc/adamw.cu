@@ -7,9 +7,9 @@
 // gradient and states are read and written once (10 bytes an element with
 // bf16 weights and 8-bit states, 22 with 32-bit ones).  At that rate an
 // element may take about 55 instructions, so the arithmetic runs on packed
-// pairs, with the hardware's approximate root and reciprocal (2^-22
-// relative, far inside the update's own rounding; squares below 2^-126 count
-// as zero).  A chunk of 2048 elements goes to a block of 8 warps, 8 consecutive
+// pairs, with the hardware's approximate reciprocal and, for 32-bit states,
+// root (2^-22 relative, far inside the update's own rounding; squares below
+// 2^-126 count as zero).  A chunk of 2048 elements goes to a block of 8 warps, 8 consecutive
 // elements to a thread; a warp then holds exactly one 256-element block of
 // the 8-bit states, whose new scales are warp-wide maxima, and no value
 // leaves registers.  The tensors' descriptors
@@ -74,7 +74,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+// The root: where it is kept in 8 bits the rounded one, else the hardware's
+// approximation.
+template <bool FP8>
 __device__ __forceinline__ float root_of(float v) {
+  if constexpr (FP8) return __fsqrt_rn(v);
   float d;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
   return d;
@@ -178,7 +182,7 @@ __device__ __forceinline__ float2 block_scale(float big) {
   big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
   if (!(big < __int_as_float(0x7f800000))) return make_float2(__int_as_float(0x7fffffff), 0.f);
   if (big < kStateMin) return make_float2(0.f, 0.f);
-  return make_float2(big * (1.0f / kE4m3Max), kE4m3Max / big);
+  return make_float2(big * (1.0f / kE4m3Max), __frcp_rn(big) * kE4m3Max);
 }
 __device__ __forceinline__ float biggest(const F8& a) {
   float m = 0.f;
@@ -190,6 +194,18 @@ __device__ __forceinline__ float biggest(const F8& a) {
   return m;
 }
 __device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
+
+// a + b, by scalar sums: packed ones are contracted with the products before
+// them.
+__device__ __forceinline__ F8 add_apart(const F8& a, const F8& b) {
+  F8 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = unpack2(a.p[j]), y = unpack2(b.p[j]);
+    r.p[j] = pack2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+  }
+  return r;
+}
 
 struct Step {           // one step's values, the same for all elements
   float gs, lr, ic1, ic2;
@@ -234,13 +250,22 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
     v = mul8(v, both(vs));
     v = mul8(v, v);
   }
-  m = fma8(m, both(a.b1), mul8(g, both(a.omb1)));
-  v = fma8(v, both(a.b2), mul8(mul8(g, both(a.omb2)), g));
+  // For 8-bit states products and sums are rounded apart, so that the
+  // roundings to 8 bits below (on which later steps depend) fall as they do
+  // for plain fp32 operations.
+  const F8 gm = mul8(g, both(a.omb1)), gv = mul8(mul8(g, both(a.omb2)), g);
+  if constexpr (FP8) {
+    m = add_apart(mul8(m, both(a.b1)), gm);
+    v = add_apart(mul8(v, both(a.b2)), gv);
+  } else {
+    m = fma8(m, both(a.b1), gm);
+    v = fma8(v, both(a.b2), gv);
+  }
   F8 root, den;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = unpack2(v.p[j]);
-    root.p[j] = pack2(root_of(f.x), root_of(f.y));
+    root.p[j] = pack2(root_of<FP8>(f.x), root_of<FP8>(f.y));
   }
   den = fma8(root, both(st.ic2), both(a.eps));
 #pragma unroll

@@ -213,6 +213,37 @@ def test_a_nan_stays_in_its_block():
                         torch.isfinite(torch.cat([s[:256], s[512:]])).all())
 
 
+def test_8_bit_states_are_those_of_plain_operations():
+    """The 8-bit roundings fall as for plain fp32 operations in the formulas'
+    order (each product and sum rounded), bit for bit over several steps: a
+    rounding that fell the other way would stay in the state."""
+    rng = np.random.default_rng(12)
+    e, _ = make(rng, 256 * 400 + 77, dtype="bf16", grad="bf16", state="fp8", master=True)
+    step = torch.zeros(2, dtype=torch.int32, device="cuda")
+    n = e["param"].numel()
+    m8, v8, ms, vs = (e[k].clone() for k in ("m", "v", "m_scale", "v_scale"))
+    blocks = lambda t: torch.cat([t, t.new_zeros(-n % BLOCK)]).reshape(-1, BLOCK)  # noqa: E731
+    for t in range(3):
+        e["grad"].copy_(torch.tensor(rng.normal(0, 0.01, size=n)))
+        g = e["grad"].float() * 0.3
+        m = (blocks(m8.float()) * ms[:, None]).reshape(-1)[:n]
+        v = (blocks(v8.float()) * vs[:, None]).square().reshape(-1)[:n]
+        m = 0.9 * m + (1 - 0.9) * g
+        r = (0.99 * v + (1 - 0.99) * g * g).sqrt()
+        run([e], step, grad_scale=torch.full((1,), 0.3, device="cuda"))
+        for k, val in (("m", m), ("v", r)):
+            b = blocks(val)
+            top = b.abs().amax(1)
+            q = b * (top.reciprocal() * 448.0)[:, None]
+            if k == "v":
+                q = torch.where((q > 0) & (q < 2.0 ** -9), 2.0 ** -9, q)
+            q = q.reshape(-1)[:n].to(torch.float8_e4m3fn)
+            sc = top * (torch.ones_like(top) / 448.0)
+            assert torch.equal(e[k].view(torch.uint8), q.view(torch.uint8)), (t, k)
+            assert torch.equal(e[k + "_scale"], sc), (t, k)
+        m8, v8, ms, vs = (e[k].clone() for k in ("m", "v", "m_scale", "v_scale"))
+
+
 def test_steps_of_an_optimizer_in_a_graph():
     """MoEAdamW over 6 steps, 4 of them replays of a captured step with the
     learning rate read from the device, against the float64 recursion."""

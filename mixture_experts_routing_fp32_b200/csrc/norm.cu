@@ -49,6 +49,7 @@ struct NormArgs {
   int several;                       // gate rows change inside the batch
   int bias_smem;                     // forward: the biases sit in shared memory too
   int w_smem;                        // backward: the running sums for w_post do
+  int swap_ring;                     // backward: the groups' exchange takes the ring's place
 };
 
 // Partial column sums a CTA leaves (arrays of [P][D] floats in this order).
@@ -337,13 +338,17 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   const int stage_bytes = 2 * (kA + kR) * pitch;
   const int o_dx = kA * pitch, o_r = 2 * kA * pitch, o_g = (2 * kA + kR) * pitch;
   const uint32_t mine = smem_addr(ring) + tid * 16;
-  // after the ring: this thread's 8 columns of w_pre and of alpha gate w_post,
-  // [kW][D] running sums for w_post, b_post (SEVERAL, where they fit; else
-  // the CTA's partial in global memory), and one [R][8 tpr] exchange buffer
-  // (R > 1)
-  const uint32_t v_pre = mine + a.stages * stage_bytes, v_post = v_pre + 2 * pitch;
-  float* w_smem = reinterpret_cast<float*>(ring + a.stages * stage_bytes + 4 * pitch);
-  float* swap = w_smem + (SEVERAL && a.w_smem ? kW * a.D : 0);
+  // after the ring: w_pre and alpha gate w_post (each thread its 8 columns,
+  // the row groups the same ones), [kW][D] running sums for w_post, b_post
+  // (SEVERAL, where they fit; else the CTA's partial in global memory), and
+  // for R > 1 one [R][8 tpr] exchange buffer (in the ring's place where the
+  // groups meet only after their last rows)
+  const int vpitch = a.tpr * 16;
+  const uint32_t v_pre = smem_addr(ring) + a.stages * stage_bytes + vec * 16,
+                 v_post = v_pre + 2 * vpitch;
+  float* w_smem = reinterpret_cast<float*>(ring + a.stages * stage_bytes + 4 * vpitch);
+  float* swap = a.swap_ring ? reinterpret_cast<float*>(ring)
+                            : w_smem + (SEVERAL && a.w_smem ? kW * a.D : 0);
   const TA* y = static_cast<const TA*>(a.y);
   const TA* dx = static_cast<const TA*>(a.dx);
   const TR* r = static_cast<const TR*>(a.r);
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   for (int i = 0; i < a.stages - 1; ++i) issue();
   // idle threads of a row's last warp hold zeros in both vectors and in
   // every tensor they weight, so they add nothing to the row's sums
-  keep(v_pre, pitch, active && a.w_pre != nullptr ? load_f8(a.w_pre + c0) : zero8f());
+  keep(v_pre, vpitch, active && a.w_pre != nullptr ? load_f8(a.w_pre + c0) : zero8f());
   uint32_t slot = mine;
   for (int seg0 = row0; seg0 < row1;) {
     const int seg1 = seg_end(seg0);
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
         if (gate != nullptr) w = mul8(w, load_f8(gate));
         if (a.w_post != nullptr) w = mul8(w, load_f8(a.w_post + c0));
       }
-      keep(v_post, pitch, w);
+      keep(v_post, vpitch, w);
     }
     for (; t < seg1; t += a.R) {
       issue();
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
         const F8 h = fma8(get(r, o_r), pack2(st.w, st.w), pack2(c, c));
         p1 = fma8(u, h, p1);
         if (GENERAL) p2 = add8(p2, u);
-        u = mul8(u, take<float>(v_pre, pitch));
+        u = mul8(u, take<float>(v_pre, vpitch));
         float m1;
         if (GENERAL && a.layer) {
           const float2 q = sum(dot8(u, h), sum8(u));
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
         const F8 yh = fma8(get(y, 0), pack2(st.y, st.y), pack2(c, c));
         s1 = fma8(d, yh, s1);
         if (GENERAL) s2 = add8(s2, d);
-        F8 e = mul8(d, take<float>(v_post, pitch));
+        F8 e = mul8(d, take<float>(v_post, vpitch));
         if (a.w_post != nullptr) {
           float m1;
           if (GENERAL && a.layer) {
@@ -715,7 +720,8 @@ int backward(NormArgs a, int P, bool bias, SumArgs& sum, cudaStream_t s) {
   const int threads = a.R * a.tpr;
   const bool general = bias || a.layer;
   const size_t stage = 2 * (size_t)(kPiece<TA> + kPiece<TR>) * threads;
-  size_t fixed = (size_t)threads * 64 + (a.R > 1 ? (size_t)threads * 32 : 0);
+  const size_t swap = a.R > 1 ? (size_t)threads * 32 : 0;
+  size_t fixed = (size_t)a.tpr * 64 + (a.several ? swap : 0);
   // two CTAs an SM share its shared memory (8 KB static and 1 KB of the
   // system's each)
   const size_t room = (threads > 512 ? kSmemLimit + 1024 : (kSmemLimit + 1024) / 2) - 9 * 1024;
@@ -727,6 +733,8 @@ int backward(NormArgs a, int P, bool bias, SumArgs& sum, cudaStream_t s) {
   // fp32 rows) are read where they are used
   a.stages = (int)std::min<size_t>(3, (room - fixed) / stage);
   if (a.stages < 2) a.stages = 0;
+  a.swap_ring = !a.several && a.stages > 0;      // (a stage is at least the buffer's size)
+  if (!a.several && !a.swap_ring) fixed += swap;
   const size_t smem = a.stages * stage + fixed;
   auto go = [&](auto k) {
     MOE_HTRY(host::allow_smem(k, kDynSmem));

@@ -26,11 +26,16 @@ class MoEBlock:
 
     def __init__(self, cfg, norm="rms", eps=1e-5, alpha=1.0, gate_len=0, resid=None,
                  device="cuda", **layer_kw):
+        if cfg.n_local_experts:
+            raise MoEError("MoEBlock: the outputs of expert shards are sums to be formed before "
+                           "the norm; use moe_block_norm after the exchange")
         self.layer = MoELayer(cfg, device=device, **layer_kw)
         c = self.layer.cfg
         act = self.layer.act_dtype
-        self.resid_dtype = act if resid is None else {"bf16": torch.bfloat16,
-                                                      "fp32": torch.float32}[resid]
+        kinds = {None: act, "bf16": torch.bfloat16, "fp32": torch.float32}
+        if resid not in kinds:
+            raise MoEError("MoEBlock: resid is 'bf16' or 'fp32', not %r" % (resid,))
+        self.resid_dtype = kinds[resid]
         make = lambda L: api.make_norm_config(  # noqa: E731
             c.T, c.D, norm=norm, dtype=act, resid=self.resid_dtype, eps=eps, alpha=alpha,
             gate_len=L)

@@ -77,3 +77,23 @@ def test_tensors_of_other_shapes_are_refused():
                  (x.t(), q.t(), torch.zeros(64))):
         with pytest.raises(C.MoEError):
             api.moe_quant_i8(*args)
+
+
+def test_rows_are_aligned_for_pairs_sooner(lib):
+    """MOE_GEMM_I8: segments of 256 rows from 512 rows per expert on (1536
+    otherwise); other values of gemm_impl are refused."""
+    for T, impl, align in ((2048, C.MOE_GEMM_I8, 256), (2047, C.MOE_GEMM_I8, 128),
+                           (2048, C.MOE_GEMM_AUTO, 128), (6144, C.MOE_GEMM_AUTO, 256)):
+        cfg = api.make_config(T, 128, 8, 2, 128, gemm_impl=impl)
+        assert api.moe_get_sizes(cfg).row_align == align, (T, impl)
+    with pytest.raises(C.MoEError):
+        api.moe_get_sizes(api.make_config(64, 128, 8, 2, 128, gemm_impl=3))
+
+
+def test_blocks_refuse_shards_and_unknown_types():
+    from mixture_experts_routing_fp32_b200 import MoEBlock
+    shard = api.make_config(64, 128, 8, 2, 128, expert_base=0, n_local_experts=4)
+    with pytest.raises(C.MoEError, match="shards"):
+        MoEBlock(shard, device="cpu")
+    with pytest.raises(C.MoEError, match="resid"):
+        MoEBlock(api.make_config(64, 128, 8, 2, 128), resid="fp8", device="cpu")

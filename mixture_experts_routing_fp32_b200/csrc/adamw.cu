@@ -78,9 +78,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
 // approximation.
 template <bool FP8>
 __device__ __forceinline__ float root_of(float v) {
-  if constexpr (FP8) return __fsqrt_rn(v);
   float d;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  if constexpr (FP8) asm("sqrt.rn.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  else asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
   return d;
 }
 __device__ __forceinline__ float recip(float v) {
@@ -189,12 +189,15 @@ __device__ __forceinline__ float biggest(const F8& a) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float2 f = unpack2(a.p[k]);
-    m = max_nan(m, max_nan(fabsf(f.x), fabsf(f.y)));
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f.x), "f"(f.y));
   }
   return m;
 }
 __device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
 
+__device__ __forceinline__ bool has_zero_byte(uint32_t w) {
+  return ((w - 0x01010101u) & ~w & 0x80808080u) != 0u;
+}
 // a + b, by scalar sums: packed ones are contracted with the products before
 // them.
 __device__ __forceinline__ F8 add_apart(const F8& a, const F8& b) {
@@ -289,14 +292,20 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
     const float2 sm = block_scale(biggest(m)), sv = block_scale(biggest(root));
     m = mul8(m, both(sm.y));
     root = mul8(root, both(sv.y));
+    uint2 qv = narrow_fp8(root);
+    // a positive root is never stored as zero (bytes that came out zero, or
+    // could have: looked at one by one only where there are such)
+    if (has_zero_byte(qv.x) || has_zero_byte(qv.y)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2(root.p[j]);
-      root.p[j] = pack2(f.x > 0.f ? fmaxf(f.x, kE4m3Least) : f.x,
-                        f.y > 0.f ? fmaxf(f.y, kE4m3Least) : f.y);
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2(root.p[j]);
+        root.p[j] = pack2(f.x > 0.f ? fmaxf(f.x, kE4m3Least) : f.x,
+                          f.y > 0.f ? fmaxf(f.y, kE4m3Least) : f.y);
+      }
+      qv = narrow_fp8(root);
     }
     store_fp8(mp + i, narrow_fp8(m), whole, left);
-    store_fp8(vp + i, narrow_fp8(root), whole, left);
+    store_fp8(vp + i, qv, whole, left);
     if ((threadIdx.x & 31) == 0 && left > 0) {
       t.ms[i / MOE_ADAMW_BLOCK] = sm.x;
       t.vs[i / MOE_ADAMW_BLOCK] = sv.x;
@@ -312,14 +321,21 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, kPerSm<FP8>) adamw_kernel(const __grid_constant__ Args a) {
+  __shared__ Step st_s;
+  __shared__ int step_s;
   pdl_begin();
-  const int step = a.step[0] + 1;
-  Step st;
-  // 1 - b^t without cancellation
-  st.ic1 = 1.0f / -expm1f((float)step * a.lb1);
-  st.ic2 = rsqrtf(-expm1f((float)step * a.lb2));
-  st.gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-  st.lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+  if (threadIdx.x == 0) {
+    const int t = a.step[0] + 1;
+    step_s = t;
+    // 1 - b^t without cancellation
+    st_s.ic1 = 1.0f / -expm1f((float)t * a.lb1);
+    st_s.ic2 = rsqrtf(-expm1f((float)t * a.lb2));
+    st_s.gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+    st_s.lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+  }
+  __syncthreads();
+  const Step st = st_s;
+  const int step = step_s;
   const int64_t total = a.first[a.n];
   for (int64_t chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
     int lo = 0, hi = a.n;                  // the last tensor with first <= chunk

@@ -202,19 +202,23 @@ quant_dispatch_kernel(const __grid_constant__ CUtensorMap mapW,
 // epilogue) to 8 bits: 16 columns a thread, 512 a warp and turn.  h is fp32,
 // where ties mean nothing, so the quotient is a product with 127 / max.
 __global__ void __launch_bounds__(kHThreads)
-quant_h_kernel(const float* h, int F, const int32_t* stats, const int32_t* tile_rows,
+quant_h_kernel(const float* h, int F, int64_t rows_max, const int32_t* stats, const int32_t* tile_rows,
                const unsigned* row_max, int8_t* hq) {
   pdl_begin();
   const int lane = threadIdx.x & 31;
   const int per = (F + 511) / 512;
-  const int64_t total = (int64_t)stats[2] * per;
   const int64_t step = (int64_t)gridDim.x * (kHThreads >> 5);
-  for (int64_t u = (int64_t)blockIdx.x * (kHThreads >> 5) + (threadIdx.x >> 5); u < total;
+  const int64_t total = (int64_t)stats[2] * per, most = rows_max * per;
+  // (a row's facts are asked for whether it is in use or not: one latency
+  // instead of three where there are few rows)
+  for (int64_t u = (int64_t)blockIdx.x * (kHThreads >> 5) + (threadIdx.x >> 5); u < most;
        u += step) {
     const int64_t r = u / per;
     const int c = (int)(u - r * per) * 512 + lane * 16;
-    if (c >= F || (int)(r % kRowTile) >= tile_rows[r / kRowTile]) continue;
+    const int held = tile_rows[r / kRowTile];
     const unsigned bits = row_max[r];
+    if (u >= total) break;
+    if (c >= F || (int)(r % kRowTile) >= held) continue;
     const float big = __uint_as_float(bits);
     const float shift = range_shift(big);
     const float inv = (bits < 0x7f800000u && bits > 0u) ? 127.0f / (big * shift) : 0.f;
@@ -484,7 +488,7 @@ int moe_expert_ffn_i8(const moe_config_t* c, const void* x, const int32_t* offse
   MOE_HTRY(host::launch("quant_h", quant_h_kernel,
                         (int)std::min<int64_t>(host::ceil_div(w.v.rows_max * host::ceil_div(c->F, 512), 8),
                                                (int64_t)sms * 8),
-                        kHThreads, 0, s, 1, h, c->F, stats, tile_rows, row_max, hq));
+                        kHThreads, 0, s, 1, h, c->F, w.v.rows_max, stats, tile_rows, row_max, hq));
   if (thin) return thin_product_of<i8::I8_STORE>(nt, w, "i8_down_thin", hq, td, td, o, q, s);
   return product<i8::I8_STORE>(c, w, "i8_down", hq, c->F, w_down, w_down_s, c->D, o, q, s);
 }

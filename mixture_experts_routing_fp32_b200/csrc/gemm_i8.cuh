@@ -612,6 +612,13 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
       int issued_parity[STAGES];
 #pragma unroll
       for (int s = 0; s < STAGES; ++s) issued_parity[s] = s < early ? 0 : -1;
+      // the same stages' tokens: the tile's first turn starts at its first
+      // row whatever else it holds
+      for (int s = 0; s < early; ++s) {
+        mbar_expect_tx(full_bar(s), KB * S::kB);
+        tma_k(base + s * S::kStage + KB * S::kA, &mapT, full_bar(s), s * KB,
+              (int)blockIdx.x / p.nN * BM, 0, 0, pol);
+      }
       bool ok = true;
       T nxt = decode_at(blockIdx.x);
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -619,17 +626,16 @@ gemm_i8_thin_kernel(const __grid_constant__ CUtensorMap mapW,
         nxt = decode_at(t + gridDim.x);
         for (int r0 = 0; r0 < d.rows && ok; r0 += NT) {
           for (int kb = 0; kb < p.nk; kb += KB) {
-            if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
-            const uint32_t fb = full_bar(stage);
-            if (early > 0) {              // weights on their way already
+            if (early > 0) {              // on its way already
               --early;
-              mbar_expect_tx(fb, KB * S::kB);
             } else {
+              if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+              const uint32_t fb = full_bar(stage);
               mbar_expect_tx(fb, S::kStage);
               load_weights(stage, kb, d.n0, d.e);
+              issued_parity[stage] = (int)phase;
+              tma_k(base + stage * S::kStage + KB * S::kA, &mapT, fb, kb, d.m0 + r0, 0, 0, pol);
             }
-            issued_parity[stage] = (int)phase;
-            tma_k(base + stage * S::kStage + KB * S::kA, &mapT, fb, kb, d.m0 + r0, 0, 0, pol);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
         }

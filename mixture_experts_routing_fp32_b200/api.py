@@ -231,11 +231,15 @@ def moe_block_norm(cfg, r, y, w_post, b_post, gate, w_pre, b_pre, r_out, x, stat
         ("stats", stats, f32, 4 * T))), "moe_block_norm")
 
 
+_norm_ws = {}      # workspace bytes by (T, D, gate_len)
+
+
 def moe_block_norm_ws_bytes(cfg) -> int:
     """Workspace of moe_block_norm_backward."""
     n = int(lib().moe_block_norm_ws_bytes(ctypes.byref(cfg)))
     if n <= 0:
         check(C.MOE_ERR_ARG, "moe_block_norm_ws_bytes")
+    _norm_ws[cfg.T, cfg.D, cfg.gate_len] = n
     return n
 
 
@@ -244,7 +248,8 @@ def moe_block_norm_backward(cfg, r_out, y, w_post, b_post, gate, w_pre, stats, d
     T, D, L, f32 = cfg.T, cfg.D, cfg.gate_len, torch.float32
     n, act, res = T * D, _TYPES[cfg.dtype], _TYPES[cfg.resid]
     g = -(-T // L) * D if L > 0 else 0
-    if ws is not None and ws.numel() < moe_block_norm_ws_bytes(cfg):
+    need = _norm_ws.get((T, D, L)) or moe_block_norm_ws_bytes(cfg)
+    if ws is not None and ws.numel() < need:
         raise MoEError("moe_block_norm_backward: the workspace is too small")
     check(lib().moe_block_norm_backward(ctypes.byref(cfg), *_args(
         "moe_block_norm_backward", stream, ("r_out", r_out, res, n), ("y", y, act, n),

@@ -49,7 +49,9 @@ struct NormArgs {
   void *dy, *dr;
   float* dgate;
   float* part;                       // partial column sums, kSlots arrays of [P][D]
+  float *dw_post, *db_post, *dw_pre, *db_pre;
   int several;                       // gate rows change inside the batch
+  int finish;                        // backward: one CTA, which writes the gradients itself
   int bias_smem;                     // forward: the biases sit in shared memory too
   int w_smem;                        // backward: the running sums for w_post do
   int swap_ring;                     // backward: the groups' exchange takes the ring's place
@@ -515,6 +517,40 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
     seg0 = seg1;
   }
   cp_wait(0);
+  if (!SEVERAL && a.finish) {
+    // one CTA held all rows: its sums are the gradients
+    auto put = [&](float* out, const F8& v) {
+      if (out == nullptr) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2(v.p[i]);
+        out[c0 + 2 * i] = f.x;
+        out[c0 + 2 * i + 1] = f.y;
+      }
+    };
+    join(s1);
+    join(p1);
+    if (GENERAL) {
+      join(s2);
+      join(p2);
+    }
+    if (g != 0 || !active) return;
+    if (a.y != nullptr) {
+      F8 dg = s1;
+      if (a.w_post != nullptr) dg = mul8(dg, load_f8(a.w_post + c0));
+      if (GENERAL && a.b_post != nullptr) dg = fma8(load_f8(a.b_post + c0), s2, dg);
+      put(a.dgate, mul8(dg, pack2(a.alpha, a.alpha)));
+      F8 w = add8(zero8f(), pack2(a.alpha, a.alpha));
+      if (a.gate_len > 0) w = mul8(w, load_f8(a.gate + c0));
+      put(a.dw_post, mul8(w, s1));
+      if (GENERAL) put(a.db_post, mul8(w, s2));
+    }
+    if (a.dx != nullptr) {
+      put(a.dw_pre, p1);
+      if (GENERAL) put(a.db_pre, p2);
+    }
+    return;
+  }
   if (!SEVERAL && a.y != nullptr) {
     join(s1);
     if (g == 0 && active) store_f8(part + S1H * arr, s1);
@@ -545,7 +581,6 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
 struct SumArgs {
   NormArgs n;
   int P, by_row;
-  float *dw_post, *db_post, *dw_pre, *db_pre;
 };
 
 __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const SumArgs s) {
@@ -592,19 +627,19 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const SumArgs s) {
   if (blockIdx.y == 0) {
     float v[4];
     const bool gate1 = a.dgate != nullptr && !a.several;
-    const bool s1 = a.y != nullptr && (s.dw_post != nullptr || gate1);
-    const bool s2 = a.y != nullptr && (s.db_post != nullptr || (gate1 && a.b_post != nullptr));
+    const bool s1 = a.y != nullptr && (a.dw_post != nullptr || gate1);
+    const bool s2 = a.y != nullptr && (a.db_post != nullptr || (gate1 && a.b_post != nullptr));
     // several gate rows: the sums already hold the gate
     const int which[4] = {s1 ? (a.several ? W1 : S1H) : -1, s2 ? (a.several ? W2 : S2H) : -1,
-                          s.dw_pre != nullptr ? P1 : -1, s.db_pre != nullptr ? P2 : -1};
+                          a.dw_pre != nullptr ? P1 : -1, a.db_pre != nullptr ? P2 : -1};
     add(which, 0, s.P, v);
     if (!in || strand != 0) return;
     const float gate = (a.gate_len > 0 && !a.several) ? a.gate[col] : 1.f;
-    if (s.dw_post != nullptr) s.dw_post[col] = a.alpha * gate * v[0];
-    if (s.db_post != nullptr) s.db_post[col] = a.alpha * gate * v[1];
+    if (a.dw_post != nullptr) a.dw_post[col] = a.alpha * gate * v[0];
+    if (a.db_post != nullptr) a.db_post[col] = a.alpha * gate * v[1];
     if (gate1) a.dgate[col] = gate_grad(v[0], v[1], col);
-    if (s.dw_pre != nullptr) s.dw_pre[col] = v[2];
-    if (s.db_pre != nullptr) s.db_pre[col] = v[3];
+    if (a.dw_pre != nullptr) a.dw_pre[col] = v[2];
+    if (a.db_pre != nullptr) a.db_pre[col] = v[3];
     return;
   }
   // The CTA that starts the gate row left its share as its tail, those that
@@ -662,12 +697,15 @@ int row_groups(int tpr, int threads) {
 // file), else two of up to 512 threads.  Row groups share a CTA's partial
 // sums, so short batches run fewer CTAs rather than CTAs of one group; with
 // short gate segments, which a CTA's groups share, each needs four rows.
+// Up to two rows per group of one gate row go to one CTA, which then writes
+// the gradients itself: a second launch costs more than a second row.
 void bwd_shape(const moe_norm_config_t* c, int* ctas, int* groups) {
   const int tpr = threads_per_row(c->D);
   const int64_t most = (int64_t)kSms * (tpr > 512 ? 1 : 2);
   int64_t R = row_groups(tpr, 512);
   if (several_rows(c)) R = std::max<int64_t>(1, std::min<int64_t>(R, c->gate_len / 4));
   *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most, host::ceil_div(c->T, R)));
+  if (!several_rows(c) && c->T <= 2 * R) *ctas = 1;
   *groups = (int)std::min<int64_t>(R, host::ceil_div(c->T, *ctas));
 }
 
@@ -719,7 +757,7 @@ int forward(NormArgs a, cudaStream_t s) {
 }
 
 template <typename TA, typename TR>
-int backward(NormArgs a, int P, bool bias, SumArgs& sum, cudaStream_t s) {
+int backward(NormArgs a, int P, bool bias, cudaStream_t s) {
   const int threads = a.R * a.tpr;
   const bool general = bias || a.layer;
   const size_t stage = 2 * (size_t)(kPiece<TA> + kPiece<TR>) * threads;
@@ -743,11 +781,14 @@ int backward(NormArgs a, int P, bool bias, SumArgs& sum, cudaStream_t s) {
     MOE_HTRY(host::allow_smem(k, kDynSmem));
     return host::launch("block_norm_bwd", k, P, threads, smem, s, 1, a);
   };
+  a.finish = P == 1 && !a.several;
   MOE_HTRY(with_flags(general, a.several != 0, [&](auto ge, auto se) {
     constexpr bool G = decltype(ge)::value, S = decltype(se)::value;
     return a.D % 256 == 0 ? go(block_norm_bwd_kernel<TA, TR, G, S, true>)
                           : go(block_norm_bwd_kernel<TA, TR, G, S, false>);
   }));
+  if (a.finish) return MOE_OK;
+  SumArgs sum{};
   sum.n = a;
   sum.P = P;
   // dgate of the gate rows that CTAs cut: by gate row where there are fewer
@@ -820,14 +861,13 @@ int moe_block_norm_backward(const moe_norm_config_t* c, const void* r_out, const
   a.stats_in = stats; a.dx = dx; a.dr_out = dr_out; a.dy = dy; a.dr = dr; a.dgate = dgate;
   a.part = static_cast<float*>(ws);
   a.several = y != nullptr && several_rows(c);
-  SumArgs sum{};
-  sum.dw_post = dw_post; sum.db_post = db_post; sum.dw_pre = dw_pre; sum.db_pre = db_pre;
+  a.dw_post = dw_post; a.db_post = db_post; a.dw_pre = dw_pre; a.db_pre = db_pre;
   int P = 0;
   bwd_shape(c, &P, &a.R);
   const bool bias = db_post != nullptr || db_pre != nullptr || (dgate != nullptr && b_post != nullptr);
-  if (c->dtype == MOE_FP32) return backward<float, float>(a, P, bias, sum, s);
-  if (c->resid == MOE_FP32) return backward<__nv_bfloat16, float>(a, P, bias, sum, s);
-  return backward<__nv_bfloat16, __nv_bfloat16>(a, P, bias, sum, s);
+  if (c->dtype == MOE_FP32) return backward<float, float>(a, P, bias, s);
+  if (c->resid == MOE_FP32) return backward<__nv_bfloat16, float>(a, P, bias, s);
+  return backward<__nv_bfloat16, __nv_bfloat16>(a, P, bias, s);
 }
 
 }  // extern "C"

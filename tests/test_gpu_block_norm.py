@@ -175,6 +175,9 @@ CASES = [
     dict(T=160, D=7168, gate_len=3, bias=True), dict(T=155, D=8192, dtype="fp32", gate_len=60,
                                                      norm="layer", bias=True),
     dict(T=150, D=8192, dtype="fp32"), dict(T=64, D=520, post=False, gate_len=9),
+    dict(T=2, D=4096, gate_len=2, norm="layer", bias=True), dict(T=16, D=256, bias=True),
+    dict(T=17, D=256, gate_len=17, bias=True), dict(T=8, D=264, y=False, bias=True),
+    dict(T=10, D=768, resid="fp32", gate_len=10), dict(T=31, D=64, post=False, gate_len=40),
     dict(T=129, D=512, y=False), dict(T=70, D=1536, y=False, norm="layer", bias=True,
                                       dtype="fp32"),
 ]

@@ -69,11 +69,6 @@ struct Args {
   const float *lr_dev, *grad_scale;
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
 // The root: where it is kept in 8 bits the rounded one, else the hardware's
 // approximation.
 template <bool FP8>
@@ -175,11 +170,8 @@ __device__ __forceinline__ void store_fp8(uint8_t* p, const uint2& u, bool whole
 // Scale of a block from its largest magnitude, and what its values are
 // multiplied by before rounding.  Not finite: everything becomes NaN.
 __device__ __forceinline__ float2 block_scale(float big) {
-  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 16));
-  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 8));
-  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 4));
-  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
-  big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  // (magnitudes order as their bits do, NaN on top)
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
   if (!(big < __int_as_float(0x7f800000))) return make_float2(__int_as_float(0x7fffffff), 0.f);
   if (big < kStateMin) return make_float2(0.f, 0.f);
   return make_float2(big * (1.0f / kE4m3Max), __frcp_rn(big) * kE4m3Max);
@@ -211,7 +203,9 @@ __device__ __forceinline__ F8 add_apart(const F8& a, const F8& b) {
 }
 
 struct Step {           // one step's values, the same for all elements
-  float gs, lr, ic1, ic2;
+  float gs, lr;
+  // m'/c1 / (sqrt(v'/c2) + eps) = m' / (sqrt(v') root_mul + root_add)
+  float root_mul, root_add;
 };
 
 // One chunk of tensor t: TP, TG the types of parameter and gradient; MASTER:
@@ -228,6 +222,7 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
   Raw<TW> rw;
   Raw<TS> rm, rv;
   float ms, vs;
+  const uint64_t block = (uint64_t)i / MOE_ADAMW_BLOCK;
   const int64_t left = t.n - i;       // elements from this thread's first on (may be negative)
   const bool whole = t.wide && left >= 8;
   if (whole) {
@@ -242,8 +237,8 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
     rv.load(vp + i, left);
   }
   if constexpr (FP8) {
-    ms = left > 0 ? t.ms[i / MOE_ADAMW_BLOCK] : 0.f;
-    vs = left > 0 ? t.vs[i / MOE_ADAMW_BLOCK] : 0.f;
+    ms = left > 0 ? t.ms[block] : 0.f;
+    vs = left > 0 ? t.vs[block] : 0.f;
   }
   const uint64_t lr = both(-st.lr * t.lr_mult), wd = both(t.decay ? a.wd : 0.f);
   const F8 g = mul8(rg.wide(), both(st.gs));
@@ -270,14 +265,14 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
     const float2 f = unpack2(v.p[j]);
     root.p[j] = pack2(root_of<FP8>(f.x), root_of<FP8>(f.y));
   }
-  den = fma8(root, both(st.ic2), both(a.eps));
+  den = fma8(root, both(st.root_mul), both(st.root_add));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = unpack2(den.p[j]);
     den.p[j] = pack2(recip(f.x), recip(f.y));
   }
   const F8 p = rw.wide();
-  const F8 up = fma8(p, wd, mul8(mul8(m, both(st.ic1)), den));
+  const F8 up = fma8(p, wd, mul8(m, den));
   const F8 w = fma8(up, lr, p);
   TP* pp = static_cast<TP*>(t.p);
   if (whole) {
@@ -307,8 +302,8 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
     store_fp8(mp + i, narrow_fp8(m), whole, left);
     store_fp8(vp + i, qv, whole, left);
     if ((threadIdx.x & 31) == 0 && left > 0) {
-      t.ms[i / MOE_ADAMW_BLOCK] = sm.x;
-      t.vs[i / MOE_ADAMW_BLOCK] = sv.x;
+      t.ms[block] = sm.x;
+      t.vs[block] = sv.x;
     }
   } else if (whole) {
     store_f8(mp + i, m);
@@ -328,8 +323,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<FP8>) adamw_kernel(const __gr
     const int t = a.step[0] + 1;
     step_s = t;
     // 1 - b^t without cancellation
-    st_s.ic1 = 1.0f / -expm1f((float)t * a.lb1);
-    st_s.ic2 = rsqrtf(-expm1f((float)t * a.lb2));
+    const float c1 = -expm1f((float)t * a.lb1);
+    st_s.root_mul = c1 * rsqrtf(-expm1f((float)t * a.lb2));
+    st_s.root_add = c1 * a.eps;
     st_s.gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
     st_s.lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
   }
@@ -337,11 +333,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<FP8>) adamw_kernel(const __gr
   const Step st = st_s;
   const int step = step_s;
   const int64_t total = a.first[a.n];
+  int lo = 0;                              // the last tensor with first <= chunk
   for (int64_t chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
-    int lo = 0, hi = a.n;                  // the last tensor with first <= chunk
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.first[mid] <= chunk) lo = mid; else hi = mid;
+    if (chunk >= a.first[lo + 1]) {
+      int hi = a.n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.first[mid] <= chunk) lo = mid; else hi = mid;
+      }
     }
     const Tensor& t = a.t[lo];
     const int64_t i = (chunk - a.first[lo]) * kChunk + threadIdx.x * 8;
@@ -407,7 +406,7 @@ extern "C" int moe_adamw(const moe_adamw_config_t* c, const moe_adamw_tensor_t* 
   if (c == nullptr || n_tensors < 0 || (n_tensors > 0 && tensors == nullptr) || step == nullptr)
     return MOE_ERR_ARG;
   if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0) ||
-      !((float)c->eps >= FLT_MIN) || !std::isfinite(c->lr) || !std::isfinite(c->weight_decay))
+      !((float)(c->eps * (1.0 - c->beta1)) >= FLT_MIN) || !std::isfinite(c->lr) || !std::isfinite(c->weight_decay))
     return MOE_ERR_ARG;
   if (host::misaligned(step, 4) || host::misaligned(lr, 4) || host::misaligned(grad_scale, 4))
     return MOE_ERR_ARG;

@@ -38,7 +38,7 @@ def test_struct_layout_matches_header():
 
 @pytest.mark.parametrize("bad", [
     dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=float("nan")), dict(eps=0.0),
-    dict(eps=1e-39),
+    dict(eps=1e-39), dict(eps=2e-38, beta1=0.9),
     dict(lr=float("inf")), dict(weight_decay=float("nan")),
 ])
 def test_bad_hyper_parameters_are_refused(lib, bad):

@@ -175,15 +175,19 @@ __device__ __forceinline__ int first_row(int T, int p, int P) {
   return (int)((int64_t)T * p / P);
 }
 
-// mean and rstd of a row held 8 values a thread (zeros in idle threads).
+// mean and rstd of a row held 8 values a thread.  Idle threads (those of a
+// row's last warp behind its end) hold the row's last 8 values again: they
+// load and compute like the others, so that nothing but sums and stores has
+// to ask which they are.
 // The variance is that of the centred values (a second sum), so a mean that
 // is large against the spread costs no digits.  (Joining each warp's own
 // centred sums instead, with one exchange, measured 166 against 142 us for
 // 16384 rows of 4096 bf16: its chain of shuffles is as long.)
 __device__ __forceinline__ float2 moments(const F8& v, bool active, const NormArgs& a,
                                           RowSum& sum) {
-  if (!a.layer) return make_float2(0.f, rsqrtf(fmaf(sum(dot8(v, v)), a.inv_d, a.eps)));
-  const float mean = sum(sum8(v)) * a.inv_d;
+  if (!a.layer)
+    return make_float2(0.f, rsqrtf(fmaf(sum(active ? dot8(v, v) : 0.f), a.inv_d, a.eps)));
+  const float mean = sum(active ? sum8(v) : 0.f) * a.inv_d;
   const F8 d = add8(v, pack2(-mean, -mean));
   return make_float2(mean, rsqrtf(fmaf(sum(active ? dot8(d, d) : 0.f), a.inv_d, a.eps)));
 }
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
   const int tid = threadIdx.x;
   const int g = a.R == 1 ? 0 : tid / a.tpr, vec = tid - g * a.tpr;
   const bool active = FULL || vec < a.nv;
-  const int c0 = active ? vec * 8 : 0;
+  const int c0 = (FULL ? vec : min(vec, a.nv - 1)) * 8;
   RowSum sum{red_s + g * 64, a.tpr >> 5, vec >> 5, tid & 31, 1 + g, a.tpr, 0};
   const int pitch = blockDim.x * 16;
   constexpr int kChunks = (kPiece<TA> + kPiece<TR>) / 16;
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
   uint32_t slot_in = mine_a;
   const uint32_t ring_end = mine_a + a.stages * stage_bytes;
   auto issue = [&] {
-    if (ahead < row1 && active) {
+    if (ahead < row1) {
       const int64_t at = (int64_t)ahead * a.D + c0;
       if (y != nullptr) fetch<TA>(slot_in, pitch, y + at);
       fetch<TR>(slot_in + r_off, pitch, r + at);
@@ -234,23 +238,21 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
     if (slot_in == ring_end) slot_in = mine_a;
   };
   for (int i = 0; i < a.stages - 1; ++i) issue();
-  if (a.w_pre != nullptr) keep(v_pre, pitch, active ? load_f8(a.w_pre + c0) : zero8f());
+  if (a.w_pre != nullptr) keep(v_pre, pitch, load_f8(a.w_pre + c0));
   if (BIAS && a.bias_smem && a.w_pre != nullptr)
-    keep(v_bpre, pitch, active && a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
+    keep(v_bpre, pitch, a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
   // alpha gate w_post and alpha gate b_post of gate row gr
   auto post_vectors = [&](int gr) {
     F8 e = fma8(zero8f(), 0ull, pack2(a.alpha, a.alpha)), eb = zero8f();
-    if (active) {
-      if (a.gate_len > 0) e = mul8(e, load_f8(a.gate + (int64_t)gr * a.D + c0));
-      if (BIAS && a.b_post != nullptr) eb = mul8(e, load_f8(a.b_post + c0));
-      if (a.w_post != nullptr) e = mul8(e, load_f8(a.w_post + c0));
-    }
+    if (a.gate_len > 0) e = mul8(e, load_f8(a.gate + (int64_t)gr * a.D + c0));
+    if (BIAS && a.b_post != nullptr) eb = mul8(e, load_f8(a.b_post + c0));
+    if (a.w_post != nullptr) e = mul8(e, load_f8(a.w_post + c0));
     keep(v_post, pitch, e);
     if (BIAS && a.bias_smem) keep(v_bpost, pitch, eb);
   };
   // alpha gate b_post and b_pre where the ring leaves no room for them
   auto post_bias = [&](int gr) {
-    if (!active || a.b_post == nullptr) return zero8f();
+    if (a.b_post == nullptr) return zero8f();
     F8 eb = mul8(load_f8(a.b_post + c0), pack2(a.alpha, a.alpha));
     return a.gate_len > 0 ? mul8(eb, load_f8(a.gate + (int64_t)gr * a.D + c0)) : eb;
   };
@@ -263,13 +265,11 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
       if (gr != gate_row) post_vectors(gate_row = gr);
     }
     cp_wait(a.stages - 1);
-    F8 v = zero8f();
     const int64_t at = (int64_t)t * a.D + c0;
     float2 my = make_float2(0.f, 1.f), mr = make_float2(0.f, 1.f);
-    if (active) v = take<TR>(slot + r_off, pitch);
+    F8 v = take<TR>(slot + r_off, pitch);
     if (y != nullptr) {
-      F8 z = zero8f();
-      if (active) z = take<TA>(slot, pitch);
+      F8 z = take<TA>(slot, pitch);
       if (a.w_post != nullptr) {
         my = moments(z, active, a, sum);
         const float c = -my.x * my.y;
@@ -287,7 +287,6 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
       } else {
         if (active) store_f8(out, v);
       }
-      if (!FULL && !active) v = zero8f();
     }
     if (a.w_pre != nullptr) {
       mr = moments(v, active, a, sum);
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
       if (BIAS)
         v = fma8(v, take<float>(v_pre, pitch),
                  a.bias_smem ? take<float>(v_bpre, pitch)
-                 : active && a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
+                 : a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
       else v = mul8(v, take<float>(v_pre, pitch));
       if (active) store_f8(static_cast<TA*>(a.x) + at, v);
     }
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   const int tid = threadIdx.x;
   const int g = a.R == 1 ? 0 : tid / a.tpr, vec = tid - g * a.tpr;
   const bool active = FULL || vec < a.nv;
-  const int c0 = active ? vec * 8 : 0;
+  const int c0 = (FULL ? vec : min(vec, a.nv - 1)) * 8;
   RowSum sum{red_s + g * 64, a.tpr >> 5, vec >> 5, tid & 31, 1 + g, a.tpr, 0};
   const int pitch = blockDim.x * 16;
   constexpr int kA = kPiece<TA> / 16, kR = kPiece<TR> / 16, kW = GENERAL ? 2 : 1;
@@ -382,15 +381,13 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   auto issue = [&] {
     if (a.stages == 0) return;
     if (ahead < row1) {
-      if (active) {
-        const int64_t at = (int64_t)ahead * a.D + c0;
-        if (y != nullptr) fetch<TA>(slot_in, pitch, y + at);
-        if (dx != nullptr) {
-          fetch<TA>(slot_in + o_dx, pitch, dx + at);
-          fetch<TR>(slot_in + o_r, pitch, r + at);
-        }
-        if (gin != nullptr) fetch<TR>(slot_in + o_g, pitch, gin + at);
+      const int64_t at = (int64_t)ahead * a.D + c0;
+      if (y != nullptr) fetch<TA>(slot_in, pitch, y + at);
+      if (dx != nullptr) {
+        fetch<TA>(slot_in + o_dx, pitch, dx + at);
+        fetch<TR>(slot_in + o_r, pitch, r + at);
       }
+      if (gin != nullptr) fetch<TR>(slot_in + o_g, pitch, gin + at);
       ahead += a.R;
     }
     cp_commit();
@@ -413,20 +410,15 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
   int t = row0 + g;
   if (t < row1) st_next = stats[t];
   for (int i = 0; i < a.stages - 1; ++i) issue();
-  // idle threads of a row's last warp hold zeros in both vectors and in
-  // every tensor they weight, so they add nothing to the row's sums
-  keep(v_pre, vpitch, active && a.w_pre != nullptr ? load_f8(a.w_pre + c0) : zero8f());
+  keep(v_pre, vpitch, a.w_pre != nullptr ? load_f8(a.w_pre + c0) : zero8f());
   uint32_t slot = mine;
   for (int seg0 = row0; seg0 < row1;) {
     const int seg1 = seg_end(seg0);
     const float* gate = a.gate_len > 0 ? a.gate + (int64_t)(seg0 / a.gate_len) * a.D + c0 : nullptr;
     if (y != nullptr) {
-      F8 w = zero8f();
-      if (active) {
-        w = add8(w, pack2(a.alpha, a.alpha));
-        if (gate != nullptr) w = mul8(w, load_f8(gate));
-        if (a.w_post != nullptr) w = mul8(w, load_f8(a.w_post + c0));
-      }
+      F8 w = add8(zero8f(), pack2(a.alpha, a.alpha));
+      if (gate != nullptr) w = mul8(w, load_f8(gate));
+      if (a.w_post != nullptr) w = mul8(w, load_f8(a.w_post + c0));
       keep(v_post, vpitch, w);
     }
     for (; t < seg1; t += a.R) {
@@ -439,7 +431,6 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
       // global memory)
       auto get = [&](auto* base, int off) -> F8 {
         using T = std::remove_cv_t<std::remove_pointer_t<decltype(base)>>;
-        if (!active) return zero8f();
         return a.stages > 0 ? take<T>(slot + off, pitch) : load_f8(base + at);
       };
       F8 d;
@@ -452,12 +443,12 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
         u = mul8(u, take<float>(v_pre, vpitch));
         float m1;
         if (GENERAL && a.layer) {
-          const float2 q = sum(dot8(u, h), sum8(u));
+          const float2 q = sum(active ? dot8(u, h) : 0.f, active ? sum8(u) : 0.f);
           m1 = -q.x * a.inv_d;
           const float m2 = -q.y * a.inv_d;
           u = add8(u, pack2(m2, m2));
         } else {
-          m1 = -sum(dot8(u, h)) * a.inv_d;
+          m1 = -sum(active ? dot8(u, h) : 0.f) * a.inv_d;
         }
         // rstd (u - m2 - h m1) + dr_out
         u = fma8(h, pack2(m1, m1), u);
@@ -476,12 +467,12 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
         if (a.w_post != nullptr) {
           float m1;
           if (GENERAL && a.layer) {
-            const float2 q = sum(dot8(e, yh), sum8(e));
+            const float2 q = sum(active ? dot8(e, yh) : 0.f, active ? sum8(e) : 0.f);
             m1 = -q.x * a.inv_d;
             const float m2 = -q.y * a.inv_d;
             e = add8(e, pack2(m2, m2));
           } else {
-            m1 = -sum(dot8(e, yh)) * a.inv_d;
+            m1 = -sum(active ? dot8(e, yh) : 0.f) * a.inv_d;
           }
           e = mul8(fma8(yh, pack2(m1, m1), e), pack2(st.y, st.y));
         }

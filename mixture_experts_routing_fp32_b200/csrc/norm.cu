@@ -200,8 +200,13 @@ __device__ __forceinline__ float2 moments(const F8& v, bool active, const NormAr
 // with BIAS, b_pre and alpha gate b_post; those with the gate are formed
 // again when the gate row changes.  FULL: D is a multiple of 256, every
 // thread of a row holds columns.
-template <typename TA, typename TR, bool BIAS, bool FULL>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs a) {
+// SMALL: blocks of up to 576 threads in at most 56 registers, so that an SM
+// holds 1168 threads of them (two rows of 4104 columns, not one; three of
+// 2568).
+constexpr int kSmallBlock = 576, kSmallThreads = 1168;
+template <typename TA, typename TR, bool BIAS, bool FULL, bool SMALL>
+__global__ void __launch_bounds__(SMALL ? kSmallBlock : kMaxThreads, SMALL ? 2 : 1)
+block_norm_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red_s[16 * 64];
   const int tid = threadIdx.x;
@@ -729,8 +734,9 @@ int forward(NormArgs a, cudaStream_t s) {
   const bool bias = a.b_post != nullptr || a.b_pre != nullptr;
   const size_t stage = (size_t)(kPiece<TA> + kPiece<TR>) * threads;
   size_t fixed = (size_t)threads * 32 * (bias ? 4 : 2);
+  const bool small = !bias && threads <= kSmallBlock;
   // 64 registers a thread: 1024 threads of an SM
-  const int per_sm = std::max(1, 1024 / threads);
+  const int per_sm = std::max(1, (small ? kSmallThreads : 1024) / threads);
   const size_t room = (kSmemLimit + 1024) / per_sm - 9 * 1024;
   // biases in shared memory only where they leave two rows' room (16384 rows
   // of 4096 bf16: 142 us with two rows and the biases, 172 with four rows and
@@ -740,10 +746,16 @@ int forward(NormArgs a, cudaStream_t s) {
   a.stages = (int)std::max<size_t>(1, std::min<size_t>(4, (room - std::min(room, fixed)) / stage));
   const size_t smem = a.stages * stage + fixed;
   const int grid = (int)std::min<int64_t>(host::ceil_div(a.T, a.R), (int64_t)sms * per_sm);
-  return with_flags(bias, a.D % 256 == 0, [&](auto b, auto f) {
-    auto k = block_norm_kernel<TA, TR, decltype(b)::value, decltype(f)::value>;
+  auto go = [&](auto k) {
     MOE_HTRY(host::allow_smem(k, kDynSmem));
     return host::launch("block_norm", k, grid, threads, smem, s, 1, a);
+  };
+  return with_flags(bias, a.D % 256 == 0, [&](auto b, auto f) {
+    constexpr bool B = decltype(b)::value, F = decltype(f)::value;
+    if constexpr (!B) {
+      if (small) return go(block_norm_kernel<TA, TR, false, F, true>);
+    }
+    return go(block_norm_kernel<TA, TR, B, F, false>);
   });
 }
 

@@ -19,8 +19,9 @@
 // Each thread copies exactly the 16-byte pieces that it reads back itself,
 // so the ring needs no barrier; the only ones are those of the row sums.
 // Of the copy rate of 6.46 TB/s the bf16 RMSNorm forms reach 91% (forward,
-// 16384 x 4096: 91 us) and 81% (backward, 8192 x 7168: 135 us); LayerNorm,
-// with twice the row sums, 58% and 48%.
+// 16384 x 4096: 92 us) and 80% (backward, 8192 x 7168: 137 us); LayerNorm
+// with biases, which has twice the row sums, 58% and 56%; fp32 rows 66-79%
+// and 55-65%.
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -51,6 +52,7 @@ struct NormArgs {
   float* part;                       // partial column sums, kSlots arrays of [P][D]
   float *dw_post, *db_post, *dw_pre, *db_pre;
   int several;                       // gate rows change inside the batch
+  int wide;                          // r_out and x (dr and dy): aligned to 32 bytes
   int finish;                        // backward: one CTA, which writes the gradients itself
   int bias_smem;                     // forward: the biases sit in shared memory too
   int w_smem;                        // backward: the running sums for w_post do
@@ -126,6 +128,17 @@ __device__ __forceinline__ void keep(uint32_t slot, int pitch, const F8& a) {
                  "f"(p.y), "f"(q.x), "f"(q.y)
                  : "memory");
   }
+}
+
+// 8 columns to global memory: fp32 in one 32-byte store where the tensors are
+// aligned to that, so that every store fills whole sectors (4096 rows of 7168
+// fp32, forward: 124 -> 104 us).
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const F8& a, int) { store_f8(p, a); }
+__device__ __forceinline__ void put8(float* p, const F8& a, int wide) {
+  if (!wide) return store_f8(p, a);
+  asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(a.p[0]), "l"(a.p[1]),
+               "l"(a.p[2]), "l"(a.p[3])
+               : "memory");
 }
 
 // Sums over the tpr threads of a row group (all get them, in the same order).
@@ -242,7 +255,7 @@ block_norm_kernel(const NormArgs a) {
     slot_in += stage_bytes;
     if (slot_in == ring_end) slot_in = mine_a;
   };
-  for (int i = 0; i < a.stages - 1; ++i) issue();
+  for (int i = 0; i < a.stages; ++i) issue();
   if (a.w_pre != nullptr) keep(v_pre, pitch, load_f8(a.w_pre + c0));
   if (BIAS && a.bias_smem && a.w_pre != nullptr)
     keep(v_bpre, pitch, a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
@@ -264,7 +277,6 @@ block_norm_kernel(const NormArgs a) {
   int gate_row = -1;
   const uint8_t* slot = mine;
   for (int t = row0; t < row1; t += a.R) {
-    issue();
     if (y != nullptr) {
       const int gr = a.gate_len > 0 ? t / a.gate_len : 0;
       if (gr != gate_row) post_vectors(gate_row = gr);
@@ -272,9 +284,13 @@ block_norm_kernel(const NormArgs a) {
     cp_wait(a.stages - 1);
     const int64_t at = (int64_t)t * a.D + c0;
     float2 my = make_float2(0.f, 1.f), mr = make_float2(0.f, 1.f);
-    F8 v = take<TR>(slot + r_off, pitch);
+    // the row leaves the ring at once, so that all of the ring is in flight
+    // while it is worked on
+    F8 v = take<TR>(slot + r_off, pitch), z = zero8f();
+    if (y != nullptr) z = take<TA>(slot, pitch);
+    __syncwarp();
+    issue();
     if (y != nullptr) {
-      F8 z = take<TA>(slot, pitch);
       if (a.w_post != nullptr) {
         my = moments(z, active, a, sum);
         const float c = -my.x * my.y;
@@ -290,7 +306,7 @@ block_norm_kernel(const NormArgs a) {
         if (active) *reinterpret_cast<uint4*>(out) = u;
         v = widen8(u);
       } else {
-        if (active) store_f8(out, v);
+        if (active) put8(out, v, a.wide);
       }
     }
     if (a.w_pre != nullptr) {
@@ -302,7 +318,7 @@ block_norm_kernel(const NormArgs a) {
                  a.bias_smem ? take<float>(v_bpre, pitch)
                  : a.b_pre != nullptr ? load_f8(a.b_pre + c0) : zero8f());
       else v = mul8(v, take<float>(v_pre, pitch));
-      if (active) store_f8(static_cast<TA*>(a.x) + at, v);
+      if (active) put8(static_cast<TA*>(a.x) + at, v, a.wide);
     }
     if (a.stats != nullptr && vec == 0)
       *reinterpret_cast<float4*>(a.stats + 4 * (int64_t)t) = make_float4(my.x, my.y, mr.x, mr.y);
@@ -333,8 +349,9 @@ block_norm_kernel(const NormArgs a) {
 // the ring only where they are used (64 registers hold 16 sums and 24
 // values).
 // GENERAL: LayerNorm, or sums for biases; else RMSNorm without them.
-template <typename TA, typename TR, bool GENERAL, bool SEVERAL, bool FULL>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormArgs a) {
+// THREADS: the most that an SM's CTAs have together.
+template <typename TA, typename TR, bool GENERAL, bool SEVERAL, bool FULL, int THREADS>
+__global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red_s[16 * 64];
   const int tid = threadIdx.x;
@@ -462,7 +479,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
       } else {
         d = gin != nullptr ? get(gin, o_g) : zero8f();
       }
-      if (active) store_f8(static_cast<TR*>(a.dr) + at, d);
+      if (active) put8(static_cast<TR*>(a.dr) + at, d, a.wide);
       if (y != nullptr) {
         const float c = -st.x * st.y;
         const F8 yh = fma8(get(y, 0), pack2(st.y, st.y), pack2(c, c));
@@ -481,7 +498,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const NormA
           }
           e = mul8(fma8(yh, pack2(m1, m1), e), pack2(st.y, st.y));
         }
-        if (active) store_f8(static_cast<TA*>(a.dy) + at, e);
+        if (active) put8(static_cast<TA*>(a.dy) + at, e, a.wide);
       }
       slot += stage_bytes;
       if (slot == ring_end) slot = mine;
@@ -688,18 +705,30 @@ int threads_per_row(int D) { return (int)(host::ceil_div(D / 8, 32) * 32); }
 int row_groups(int tpr, int threads) {
   return std::max(1, std::min(threads / tpr, tpr == 32 ? 16 : 15));
 }
-// The backward's CTAs and their row groups.  An SM holds one CTA when a row
-// takes more than half of its threads (the column sums fill the register
-// file), else two of up to 512 threads.  Row groups share a CTA's partial
+// Threads of the backward that share an SM.  LayerNorm's 32 column sums a
+// thread want 80 registers (with 64 they spill: 16384 rows of 4104 bf16 349
+// -> 249 us, of 768 (twice as many) 89 -> 70); fp32 rows, whose rings are
+// short, want the threads (4096 fp32: 191 us against 251), and get the
+// registers only where a row's threads leave them.
+int sm_threads(bool layer, bool bf16) { return layer && bf16 ? 768 : 1024; }
+// CTAs an SM holds: more than three leave more partial sums than they gain
+// (65536 rows of 256, gate rows of 16: 73 us with up to three, 88 with two,
+// 127 with eight).
+int bwd_ctas(int sm_threads, int threads) {
+  return std::max(1, std::min(3, sm_threads / threads));
+}
+// The backward's CTAs and their row groups: up to half of an SM's threads a
+// CTA, or one row where that takes more.  Row groups share a CTA's partial
 // sums, so short batches run fewer CTAs rather than CTAs of one group; with
 // short gate segments, which a CTA's groups share, each needs four rows.
 // Up to two rows per group of one gate row go to one CTA, which then writes
 // the gradients itself: a second launch costs more than a second row.
 void bwd_shape(const moe_norm_config_t* c, int* ctas, int* groups) {
   const int tpr = threads_per_row(c->D);
-  const int64_t most = (int64_t)kSms * (tpr > 512 ? 1 : 2);
-  int64_t R = row_groups(tpr, 512);
+  const int on_sm = sm_threads(c->norm == MOE_LAYERNORM, c->dtype == MOE_BF16);
+  int64_t R = row_groups(tpr, on_sm / 2);
   if (several_rows(c)) R = std::max<int64_t>(1, std::min<int64_t>(R, c->gate_len / 4));
+  const int64_t most = (int64_t)kSms * bwd_ctas(on_sm, (int)R * tpr);
   *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most, host::ceil_div(c->T, R)));
   if (!several_rows(c) && c->T <= 2 * R) *ctas = 1;
   *groups = (int)std::min<int64_t>(R, host::ceil_div(c->T, *ctas));
@@ -714,8 +743,8 @@ NormArgs args_of(const moe_norm_config_t* c) {
   return a;
 }
 template <typename... P>
-bool any_misaligned(P... p) {
-  return (host::misaligned(p, 16) || ...);
+bool any_misaligned(uintptr_t to, P... p) {
+  return (host::misaligned(p, to) || ...);
 }
 
 // Calls f with the template's truth values for two run-time ones.
@@ -769,7 +798,9 @@ int backward(NormArgs a, int P, bool bias, cudaStream_t s) {
   size_t fixed = (size_t)a.tpr * 64 + (a.several ? swap : 0);
   // two CTAs an SM share its shared memory (8 KB static and 1 KB of the
   // system's each)
-  const size_t room = (threads > 512 ? kSmemLimit + 1024 : (kSmemLimit + 1024) / 2) - 9 * 1024;
+  const int ctas = bwd_ctas(sm_threads(a.layer, sizeof(TA) == 2), threads);
+  const int on_sm = ctas * threads;
+  const size_t room = (kSmemLimit + 1024) / ctas - 9 * 1024;
   // the running sums for w_post where a ring of two rows still fits
   const size_t w_bytes = (general ? 2 : 1) * (size_t)a.D * 4;
   a.w_smem = a.several && fixed + w_bytes + 2 * stage <= room;
@@ -788,8 +819,14 @@ int backward(NormArgs a, int P, bool bias, cudaStream_t s) {
   a.finish = P == 1 && !a.several;
   MOE_HTRY(with_flags(general, a.several != 0, [&](auto ge, auto se) {
     constexpr bool G = decltype(ge)::value, S = decltype(se)::value;
-    return a.D % 256 == 0 ? go(block_norm_bwd_kernel<TA, TR, G, S, true>)
-                          : go(block_norm_bwd_kernel<TA, TR, G, S, false>);
+    auto full = [&](auto n) {
+      constexpr int N = G ? decltype(n)::value : kMaxThreads;
+      return a.D % 256 == 0 ? go(block_norm_bwd_kernel<TA, TR, G, S, true, N>)
+                            : go(block_norm_bwd_kernel<TA, TR, G, S, false, N>);
+    };
+    if (on_sm <= 768) return full(std::integral_constant<int, 768>{});
+    if (on_sm <= 896) return full(std::integral_constant<int, 896>{});
+    return full(std::integral_constant<int, kMaxThreads>{});
   }));
   if (a.finish) return MOE_OK;
   SumArgs sum{};
@@ -825,11 +862,12 @@ int moe_block_norm(const moe_norm_config_t* c, const void* r, const void* y,
     return MOE_ERR_ARG;
   if ((b_post && !w_post) || (b_pre && !w_pre) || (w_pre != nullptr) != (x != nullptr))
     return MOE_ERR_ARG;
-  if (any_misaligned(r, y, w_post, b_post, gate, w_pre, b_pre, r_out, x, stats)) return MOE_ERR_ARG;
+  if (any_misaligned(16, r, y, w_post, b_post, gate, w_pre, b_pre, r_out, x, stats)) return MOE_ERR_ARG;
   NormArgs a = args_of(c);
   if (y == nullptr) a.gate_len = 0;
   a.r = r; a.y = y; a.w_post = w_post; a.b_post = b_post; a.gate = gate; a.w_pre = w_pre;
   a.b_pre = b_pre; a.r_out = r_out; a.x = x; a.stats = stats;
+  a.wide = !any_misaligned(32, r_out, x);
   if (c->dtype == MOE_FP32) return forward<float, float>(a, s);
   if (c->resid == MOE_FP32) return forward<__nv_bfloat16, float>(a, s);
   return forward<__nv_bfloat16, __nv_bfloat16>(a, s);
@@ -857,13 +895,14 @@ int moe_block_norm_backward(const moe_norm_config_t* c, const void* r_out, const
   if ((b_post && !w_post) || (dw_post && !w_post) || (db_post && !w_post) || (dgate && !gate) ||
       ((dw_pre || db_pre) && !w_pre))
     return MOE_ERR_ARG;
-  if (any_misaligned(r_out, y, w_post, b_post, gate, w_pre, stats, dx, dr_out, dy, dr, dgate, ws))
+  if (any_misaligned(16, r_out, y, w_post, b_post, gate, w_pre, stats, dx, dr_out, dy, dr, dgate, ws))
     return MOE_ERR_ARG;
   NormArgs a = args_of(c);
   if (y == nullptr) a.gate_len = 0;
   a.r = r_out; a.y = y; a.w_post = w_post; a.b_post = b_post; a.gate = gate; a.w_pre = w_pre;
   a.stats_in = stats; a.dx = dx; a.dr_out = dr_out; a.dy = dy; a.dr = dr; a.dgate = dgate;
   a.part = static_cast<float*>(ws);
+  a.wide = !any_misaligned(32, dy, dr);
   a.several = y != nullptr && several_rows(c);
   a.dw_post = dw_post; a.db_post = db_post; a.dw_pre = dw_pre; a.db_pre = db_pre;
   int P = 0;

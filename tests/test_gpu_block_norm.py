@@ -275,3 +275,54 @@ def test_graphs_and_streams():
     assert torch.equal(r_out, want_r) and torch.equal(x, want_x)
     for k in o:
         assert torch.equal(o[k], want[k]), k
+
+# Each register budget of the general backward, one to three CTAs an SM.  Up
+# to 7 rows in sequence per block here: 7 roundings, 10 partials and 5 levels
+# stay below the 32 that the column sums' tolerance counts.
+@pytest.mark.parametrize("kw", [
+    dict(T=900, D=2048, norm="layer", bias=True), dict(T=900, D=2304, norm="layer", gate_len=30),
+    dict(T=1000, D=2312, bias=True), dict(T=900, D=6152, norm="layer", gate_len=1000),
+    dict(T=500, D=6152, norm="layer", bias=True, resid="fp32", gate_len=9),
+    dict(T=500, D=6152, norm="layer", bias=True, dtype="fp32"),
+    dict(T=300, D=7176, norm="layer", bias=True), dict(T=1000, D=1000, dtype="fp32", bias=True),
+    dict(T=2000, D=72, norm="layer", bias=True, gate_len=4),
+], ids=lambda k: "-".join("%s" % v for v in k.values()))
+def test_the_backwards_block_shapes(kw):
+    case = Case(**kw)
+    r_out, x, stats = case.forward()
+    case.check_forward(r_out, x)
+    case.check_backward(r_out, case.backward(r_out, stats))
+
+
+@pytest.mark.parametrize("D", [264, 4096])
+def test_rows_aligned_to_16_bytes_only(D):
+    """Tensors that start 16 bytes behind a 32-byte boundary: the same bits."""
+    import mixture_experts_routing_fp32_b200 as moe
+    T = 67
+    case = Case(T, D, dtype="fp32", gate_len=T)
+    t = case.t
+
+    def step(off):
+        def at(like):
+            flat = torch.full((like.numel() + 8,), GUARD, device="cuda")
+            view = flat[off:off + like.numel()].view_as(like)
+            assert view.data_ptr() % 32 == (16 if off == 4 else 0)
+            return view, flat
+
+        (r_out, f0), (x, f1), (dy, f2), (dr, f3) = (at(t[k]) for k in ("r", "y", "y", "r"))
+        y, _ = at(t["y"])
+        y.copy_(t["y"])
+        stats = torch.empty(T, 4, device="cuda")
+        moe.moe_block_norm(case.nc, t["r"], y, t["w_post"], None, t["gate"], t["w_pre"], None,
+                           r_out, x, stats)
+        ws = torch.empty(moe.moe_block_norm_ws_bytes(case.nc), dtype=torch.uint8, device="cuda")
+        moe.moe_block_norm_backward(case.nc, r_out, y, t["w_post"], None, t["gate"], t["w_pre"],
+                                    stats, case.dx, case.dr_out, dy, dr, None, None, None, None,
+                                    None, ws)
+        torch.cuda.synchronize()
+        for f in (f0, f1, f2, f3):
+            assert bool((f[:off] == GUARD).all()) and bool((f[off + T * D:] == GUARD).all())
+        return r_out, x, dy, dr
+
+    for a, b in zip(step(0), step(4)):
+        assert torch.equal(a, b)

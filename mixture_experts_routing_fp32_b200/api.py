@@ -231,7 +231,11 @@ def moe_block_norm(cfg, r, y, w_post, b_post, gate, w_pre, b_pre, r_out, x, stat
         ("stats", stats, f32, 4 * T))), "moe_block_norm")
 
 
-_norm_ws = {}      # workspace bytes by (T, D, gate_len)
+_norm_ws = {}      # workspace bytes by _norm_key
+
+
+def _norm_key(cfg):
+    return cfg.T, cfg.D, cfg.gate_len, cfg.norm, cfg.dtype, cfg.resid
 
 
 def moe_block_norm_ws_bytes(cfg) -> int:
@@ -239,7 +243,7 @@ def moe_block_norm_ws_bytes(cfg) -> int:
     n = int(lib().moe_block_norm_ws_bytes(ctypes.byref(cfg)))
     if n <= 0:
         check(C.MOE_ERR_ARG, "moe_block_norm_ws_bytes")
-    _norm_ws[cfg.T, cfg.D, cfg.gate_len] = n
+    _norm_ws[_norm_key(cfg)] = n
     return n
 
 
@@ -248,7 +252,7 @@ def moe_block_norm_backward(cfg, r_out, y, w_post, b_post, gate, w_pre, stats, d
     T, D, L, f32 = cfg.T, cfg.D, cfg.gate_len, torch.float32
     n, act, res = T * D, _TYPES[cfg.dtype], _TYPES[cfg.resid]
     g = -(-T // L) * D if L > 0 else 0
-    need = _norm_ws.get((T, D, L)) or moe_block_norm_ws_bytes(cfg)
+    need = _norm_ws.get(_norm_key(cfg)) or moe_block_norm_ws_bytes(cfg)
     if ws is not None and ws.numel() < need:
         raise MoEError("moe_block_norm_backward: the workspace is too small")
     check(lib().moe_block_norm_backward(ctypes.byref(cfg), *_args(

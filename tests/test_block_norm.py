@@ -86,6 +86,21 @@ def test_workspace_grows_with_gate_rows(lib):
     assert many == 2 * one > 0
 
 
+def test_workspaces_of_other_norms_and_types_are_not_mixed_up(lib):
+    """Norm, type and shape each have their say in the workspace: one that
+    fits one configuration is refused for another that needs more."""
+    import torch
+    kinds = [("rms", "bf16"), ("layer", "bf16"), ("layer", "fp32")]
+    for D in (2048, 2816, 4096):
+        configs = [api.make_norm_config(16384, D, norm=n, dtype=d) for n, d in kinds]
+        sizes = [api.moe_block_norm_ws_bytes(c) for c in configs]
+        for c, size in zip(configs, sizes):
+            ws = torch.empty(size - 1, dtype=torch.uint8)
+            with pytest.raises(C.MoEError, match="workspace"):
+                api.moe_block_norm_backward(c, *[None] * 16, ws)
+    assert len(set(sizes)) > 1
+
+
 @pytest.mark.parametrize("norm", ["rms", "layer"])
 @pytest.mark.parametrize("post,gate_len,y", [(True, 2, True), (False, 0, True), (True, 5, False)])
 def test_reference_gradients_against_differences(norm, post, gate_len, y):

@@ -282,11 +282,11 @@ def adamw_table(entries) -> AdamwTable:
     `param`, `grad`, `m`, `v` (contiguous CUDA tensors of the same length;
     m and v fp32, or float8_e4m3fn with `m_scale` and `v_scale`, fp32 with
     one element per 256) and, if wanted, `master` (fp32), `lr_mult` (1.0)
-    and `decay` (True)."""
+    and `decay` (True).  What a step writes overlaps nothing else."""
     types = {torch.float32: C.MOE_FP32, torch.bfloat16: C.MOE_BF16}
     entries = [dict(e) for e in entries]
     arr = (AdamwTensor * max(1, len(entries)))()
-    device = None
+    device, ranges = None, []
     for a, e in zip(arr, entries):
         p, m = e["param"], e["m"]
         n, fp8 = p.numel(), m.dtype == torch.float8_e4m3fn
@@ -310,9 +310,17 @@ def adamw_table(entries) -> AdamwTable:
             if t.device != device:
                 raise MoEError("adamw_table: tensors on %s and %s" % (device, t.device))
             setattr(a, k, t.data_ptr())
+            if count:
+                ranges.append((t.data_ptr(), t.data_ptr() + count * t.element_size(), k))
         a.n, a.dtype, a.grad_dtype = n, types[p.dtype], types[e["grad"].dtype]
         a.state = C.MOE_STATE_FP8 if fp8 else C.MOE_STATE_FP32
         a.decay, a.lr_mult, a.reserved = int(bool(e.get("decay", True))), e.get("lr_mult", 1.0), 0
+    end, written = 0, 0           # of all ranges so far, of the written ones
+    for lo, hi, k in sorted(ranges):
+        if lo < (written if k == "grad" else end):
+            raise MoEError("adamw_table: %s overlaps another tensor of the step" % k)
+        end = max(end, hi)
+        written = written if k == "grad" else max(written, hi)
     return AdamwTable(arr, len(entries), device, entries)
 
 

@@ -319,12 +319,12 @@ def test_tensors_that_overlap_are_refused():
     pool = torch.zeros(4096, device="cuda")
     names = ("param", "grad", "m", "v")
     at = lambda *starts: {k: pool[s:s + 512] for k, s in zip(names, starts)}  # noqa: E731
-    ok = [at(0, 512, 1024, 1536), at(2048, 512, 2560, 3072)]
+    ok = [at(0, 512, 1024, 1536), at(2048, 512, 2560, 3200)]
     moe.moe_adamw(moe.make_adamw_config(), moe.adamw_table(ok),
                   torch.zeros(2, dtype=torch.int32, device="cuda"))
     for bad in ([ok[0], ok[0]], [at(0, 512, 1024, 1024)], [at(0, 0, 1024, 1536)],
                 [at(0, 512, 1024, 1280)], [ok[0], at(2048, 3584, 2560, 100)],
-                [ok[0], at(2048, 1500, 2560, 3072)]):
+                [ok[0], at(2048, 1500, 2560, 3200)]):
         with pytest.raises(moe.MoEError, match="overlaps"):
             moe.adamw_table(bad)
     torch.cuda.synchronize()

@@ -188,21 +188,24 @@ __device__ __forceinline__ int first_row(int T, int p, int P) {
   return (int)((int64_t)T * p / P);
 }
 
-// mean and rstd of a row held 8 values a thread.  Idle threads (those of a
-// row's last warp behind its end) hold the row's last 8 values again: they
-// load and compute like the others, so that nothing but sums and stores has
-// to ask which they are.
-// The variance is that of the centred values (a second sum), so a mean that
-// is large against the spread costs no digits.  (Joining each warp's own
-// centred sums instead, with one exchange, measured 166 against 142 us for
-// 16384 rows of 4096 bf16: its chain of shuffles is as long.)
-__device__ __forceinline__ float2 moments(const F8& v, bool active, const NormArgs& a,
-                                          RowSum& sum) {
-  if (!a.layer)
-    return make_float2(0.f, rsqrtf(fmaf(sum(active ? dot8(v, v) : 0.f), a.inv_d, a.eps)));
-  const float mean = sum(active ? sum8(v) : 0.f) * a.inv_d;
-  const F8 d = add8(v, pack2(-mean, -mean));
-  return make_float2(mean, rsqrtf(fmaf(sum(active ? dot8(d, d) : 0.f), a.inv_d, a.eps)));
+// mean and rstd of a row held 8 values a thread; v is left without its mean.
+// Idle threads (those of a row's last warp behind its end) hold the row's
+// last 8 values again: they load and compute like the others, so that nothing
+// but sums and stores has to ask which they are.
+// The variance is that of the centred values (a second sum), and these are
+// what rstd multiplies: v rstd - mean rstd in one step would round the
+// second term, 2^-24 of the mean in units of the spread.  The mean is a
+// quotient, not a product with 1 / D, so that rows whose sum and mean are
+// fp32 values are centred exactly.  (Joining each warp's own centred sums
+// instead, with one exchange, measured 166 against 142 us for 16384 rows of
+// 4096 bf16: its chain of shuffles is as long.)
+__device__ __forceinline__ float2 centre(F8& v, bool active, const NormArgs& a, RowSum& sum) {
+  float mean = 0.f;
+  if (a.layer) {
+    mean = __fdiv_rn(sum(active ? sum8(v) : 0.f), (float)a.D);
+    v = add8(v, pack2(-mean, -mean));
+  }
+  return make_float2(mean, rsqrtf(fmaf(sum(active ? dot8(v, v) : 0.f), a.inv_d, a.eps)));
 }
 
 // ---------------------------------------------------------------------------
@@ -292,9 +295,8 @@ block_norm_kernel(const NormArgs a) {
     issue();
     if (y != nullptr) {
       if (a.w_post != nullptr) {
-        my = moments(z, active, a, sum);
-        const float c = -my.x * my.y;
-        z = fma8(z, pack2(my.y, my.y), pack2(c, c));
+        my = centre(z, active, a, sum);
+        z = mul8(z, pack2(my.y, my.y));
       }
       if (BIAS) v = add8(v, a.bias_smem ? take<float>(v_bpost, pitch) : post_bias(gate_row));
       v = fma8(z, take<float>(v_post, pitch), v);
@@ -310,9 +312,8 @@ block_norm_kernel(const NormArgs a) {
       }
     }
     if (a.w_pre != nullptr) {
-      mr = moments(v, active, a, sum);
-      const float c = -mr.x * mr.y;
-      v = fma8(v, pack2(mr.y, mr.y), pack2(c, c));
+      mr = centre(v, active, a, sum);
+      v = mul8(v, pack2(mr.y, mr.y));
       if (BIAS)
         v = fma8(v, take<float>(v_pre, pitch),
                  a.bias_smem ? take<float>(v_bpre, pitch)
@@ -427,6 +428,11 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const NormArgs 
       for (int k = 1; k < a.R; ++k) v = add8(v, load_f8(swap + (k * a.tpr + vec) * 8));
   };
 
+  // (v - mean) rstd, as the forward forms it; RMSNorm's mean is 0
+  auto normal = [&](F8 v, float mean, float rstd) {
+    if (GENERAL) v = add8(v, pack2(-mean, -mean));
+    return mul8(v, pack2(rstd, rstd));
+  };
   const float4* stats = reinterpret_cast<const float4*>(a.stats_in);
   float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
   int t = row0 + g;
@@ -458,8 +464,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const NormArgs 
       F8 d;
       if (dx != nullptr) {
         F8 u = get(dx, o_dx);
-        const float c = -st.z * st.w;
-        const F8 h = fma8(get(r, o_r), pack2(st.w, st.w), pack2(c, c));
+        const F8 h = normal(get(r, o_r), st.z, st.w);
         p1 = fma8(u, h, p1);
         if (GENERAL) p2 = add8(p2, u);
         u = mul8(u, take<float>(v_pre, vpitch));
@@ -481,8 +486,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const NormArgs 
       }
       if (active) put8(static_cast<TR*>(a.dr) + at, d, a.wide);
       if (y != nullptr) {
-        const float c = -st.x * st.y;
-        const F8 yh = fma8(get(y, 0), pack2(st.y, st.y), pack2(c, c));
+        const F8 yh = normal(get(y, 0), st.x, st.y);
         s1 = fma8(d, yh, s1);
         if (GENERAL) s2 = add8(s2, d);
         F8 e = mul8(d, take<float>(v_post, vpitch));

@@ -326,3 +326,68 @@ def test_rows_aligned_to_16_bytes_only(D):
 
     for a, b in zip(step(0), step(4)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,resid", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("D", [264, 768, 4096, 7168])
+def test_layer_norm_of_rows_with_a_large_mean(D, dtype, resid):
+    """Rows of integers whose sum is exact in fp32 (below 2^24) and divides
+    by D: their mean is exact, and so are the values behind it.  A constant
+    row normalises to zeros, exactly, so that x = b_pre, r_out = r + alpha
+    gate b_post and the products with the normalised row vanish.  Rows of
+    c +- 1 (as many of each) have variance 1: rstd is within 5 U (1 / D, the
+    sum with eps, its root within 2 units), the value then takes two products
+    and a sum: 16 U of |rstd w| + |b| covers it, whatever the mean is."""
+    import mixture_experts_routing_fp32_b200 as moe
+    big = 128.0 if dtype == "bf16" else 1000.0           # c +- 1 is a bf16 value
+    rows = np.array([[big, big], [-big, -big], [big + 1, big - 1], [-big - 1, 1 - big],
+                     [3.0, 3.0], [1.0, -1.0]])
+    y = np.tile(rows, (1, D // 2))
+    const, T = np.array([0, 1, 4]), len(rows)
+    case = Case(T, D, norm="layer", dtype=dtype, resid=resid, gate_len=2, bias=True,
+                inputs={"y": y, "r": y})
+    t, p, a = case.t, case.p, case.c["alpha"]
+    mean = y.mean(1, keepdims=True)
+    rstd = 1.0 / np.sqrt(y.var(1, keepdims=True) + 1e-5)
+    hat = (y - mean) * rstd
+    # x = N(r) alone
+    x, stats = torch.empty_like(t["y"]), torch.empty(T, 4, device="cuda")
+    nc = moe.make_norm_config(T, D, norm="layer", dtype=dtype, resid=resid, eps=1e-5)
+    moe.moe_block_norm(nc, t["r"], None, None, None, None, t["w_pre"], t["b_pre"], None, x, stats)
+    assert np.array_equal(down(stats[:, 2]), mean[:, 0])
+    assert torch.equal(x[const], t["b_pre"].to(x.dtype).expand(3, D))
+    ref = hat * p["w_pre"] + p["b_pre"]
+    terms = 16 * U * (rstd * np.abs(p["w_pre"]) + np.abs(p["b_pre"]))
+    terms[const] = 0.0
+    close(x, ref, half_step(x.dtype) * np.abs(ref) * (1 + 2.0 ** -7) + terms, "x")
+    # the norm behind a block (alpha gate rounds once more, the sum with r too)
+    r_out, _, st = case.forward(pre=False)
+    assert np.array_equal(down(st[:, 0]), mean[:, 0])
+    e = a * R.gate_rows(case.c, p["gate"])
+    ref = p["r"] + e * (hat * p["w_post"] + p["b_post"])
+    spread = np.where(np.isin(np.arange(T), const)[:, None], 0.0, rstd)
+    terms = 16 * U * np.abs(e) * (spread * np.abs(p["w_post"]) + np.abs(p["b_post"]))
+    close(r_out, ref, (half_step(r_out.dtype) * (1 + 2.0 ** -7) + 2 * U) * np.abs(ref)
+          + 2 * U * np.abs(p["r"]) + terms, "r_out")
+    # constant rows alone: nothing but the biases' gradients has a column sum
+    keep = torch.tensor(const, device="cuda")
+    few = moe.make_norm_config(3, D, norm="layer", dtype=dtype, resid=resid, eps=1e-5, alpha=a)
+    o = {k: torch.full((D,), GUARD, device="cuda") for k in ("dw_post", "db_post", "dw_pre",
+                                                             "db_pre")}
+    dy, dr = torch.empty_like(t["y"][:3]), torch.empty_like(t["r"][:3])
+    stats = torch.cat([stats[keep][:, 2:]] * 2, 1)
+    dx, dr_out = case.dx[:3].contiguous(), case.dr_out[:3].contiguous()
+    ws = torch.empty(moe.moe_block_norm_ws_bytes(few), dtype=torch.uint8, device="cuda")
+    moe.moe_block_norm_backward(few, t["r"][keep], t["y"][keep], t["w_post"], t["b_post"], None,
+                                t["w_pre"], stats, dx, dr_out, dy, dr, o["dw_post"],
+                                o["db_post"], None, o["dw_pre"], o["db_pre"], ws)
+    assert not o["dw_pre"].any() and not o["dw_post"].any()
+    u = down(dx) * p["w_pre"]
+    s = 1e-5 ** -0.5
+    d = down(dr_out) + s * (u - u.mean(1, keepdims=True))
+    big_d = np.abs(down(dr_out)).max(1, keepdims=True) + 2 * s * np.abs(u).max(1, keepdims=True)
+    close(dr, d, half_step(dr.dtype) * np.abs(d) * (1 + 2.0 ** -7) + 64 * U * big_d, "dr")
+    dz = a * d * p["w_post"]
+    ref = s * (dz - dz.mean(1, keepdims=True))
+    big_y = s * a * np.abs(p["w_post"]).max() * 2 * big_d
+    close(dy, ref, half_step(dy.dtype) * np.abs(ref) * (1 + 2.0 ** -7) + 64 * U * big_y, "dy")

@@ -572,7 +572,7 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* r_out, con
  *   g  = grad * grad_scale
  *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
  *   p' = p - lr ((m'/(1-beta1^t)) / (sqrt(v'/(1-beta2^t)) + eps) + weight_decay p)
- * in fp32 (v' below 2^-126 counts as zero in the root).  Hyper-parameters are
+ * in fp32, subnormal v' included.  Hyper-parameters are
  * double so that 1 - beta keeps its digits; 0 <= beta < 1 and
  * eps (1 - beta1) >= 2^-126.
  */

@@ -8,8 +8,9 @@
 // bf16 weights and 8-bit states, 22 with 32-bit ones).  At that rate an
 // element may take about 55 instructions, so the arithmetic runs on packed
 // pairs, with the hardware's approximate reciprocal and, for 32-bit states,
-// root (2^-22 relative, far inside the update's own rounding; squares below
-// 2^-126 count as zero).  A chunk of 2048 elements goes to a block of 8 warps, 8 consecutive
+// root (2^-22 relative, far inside the update's own rounding).  The root
+// takes subnormal v: flushed to zero they would leave m' / eps, an update of
+// any size where eps is small.  A chunk of 2048 elements goes to a block of 8 warps, 8 consecutive
 // elements to a thread; a warp then holds exactly one 256-element block of
 // the 8-bit states, whose new scales are warp-wide maxima, and no value
 // leaves registers.  The tensors' descriptors
@@ -74,8 +75,8 @@ struct Args {
 template <bool FP8>
 __device__ __forceinline__ float root_of(float v) {
   float d;
-  if constexpr (FP8) asm("sqrt.rn.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
-  else asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  if constexpr (FP8) asm("sqrt.rn.f32 %0, %1;" : "=f"(d) : "f"(v));
+  else asm("sqrt.approx.f32 %0, %1;" : "=f"(d) : "f"(v));
   return d;
 }
 __device__ __forceinline__ float recip(float v) {

@@ -328,3 +328,25 @@ def test_tensors_that_overlap_are_refused():
         with pytest.raises(moe.MoEError, match="overlaps"):
             moe.adamw_table(bad)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", [dict(), dict(state="fp8"), dict(dtype="bf16", master=True)],
+                         ids=lambda k: "-".join(map(str, k.values())) or "fp32")
+def test_small_eps_and_small_gradients(kind):
+    """eps far below the smallest normal root (2^-63), gradients around and
+    below it: the step still is one of about lr.  v' is subnormal there, so
+    its terms are off by half of 2^-149 each (at most three of them), which
+    the root halves: up to 2^-149 / v' of the update."""
+    rng = np.random.default_rng(13)
+    hp = dict(HP, eps=1e-25)
+    for size in (1e-17, 3e-18, 1e-18, 1e-19, 1e-20):
+        e, _ = make(rng, 700, fresh=True, **kind)
+        e["grad"].copy_(torch.tensor(size * rng.choice([-1, 1], size=700)
+                                     * rng.uniform(0.5, 1.0, size=700)))
+        step = torch.zeros(2, dtype=torch.int32, device="cuda")
+        want = expected(e, 1, hp=hp)
+        run([e], step, hp=hp)
+        update = np.abs(want["m"]) / 0.1 / (np.sqrt(want["v"] / (1 - 0.99)) + 1e-25)
+        assert (np.abs(update - 1.0) < 1e-3).all()
+        tol = want["tol_p"] + HP["lr"] * update * 2.0 ** -149 / want["v"]
+        within(e["master"] if "master" in e else e["param"], want["p"], tol, "size %g" % size)

@@ -290,3 +290,36 @@ def test_a_block_served_in_8_bits():
     # x, h and both weights are each off by 4 / 127 / sqrt(12) = 0.9% of
     # their spread (h, a product of two, by up to three times that): under 5%
     assert float((a - b).norm() / a.norm()) < 0.05
+
+
+@pytest.mark.parametrize("T", [1, 200])
+@pytest.mark.parametrize("c", [61, 15])
+def test_h_is_quantised_as_rows_are(T, c):
+    """q(h) is moe_quant_i8's, ties included.  The layer is built so that h is
+    known exactly: gates of 128 (whose sigmoid is 1 in fp32) times integers,
+    h = 128 (2 k + 1) c beside a largest value of 128 * 254 c, so that every
+    quotient 127 h / max = k + 1/2 is a tie, and the outputs read q(h) back:
+    one weight of 1 per output, a scale of 1 / s(h)."""
+    import mixture_experts_routing_fp32_b200 as moe
+    D = F = 128
+    k = torch.randperm(127, generator=torch.Generator().manual_seed(c)).double()
+    b = torch.cat([torch.tensor([254.0 * c], dtype=torch.float64), (2 * k + 1) * c])
+    b[1::2] *= -1
+    x = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = 127.0, 1.0                     # s(x) = 1, q(x) = x
+    w13 = torch.zeros(2, 2 * F, D, dtype=torch.int8)
+    w13[:, :F, :2] = 1                                # a = 128
+    hi = torch.round(b / 127)
+    w13[:, F:, 0], w13[:, F:, 1] = hi.to(torch.int8), (b - 127 * hi).to(torch.int8)
+    wd = torch.eye(F, dtype=torch.int8).repeat(2, 1, 1)
+    layer = moe.MoEInt8Layer(moe.make_config(T, D, 2, 1, F))
+    layer.set_weights(w13.cuda(), torch.ones(2, 2 * F, device="cuda"), wd.cuda(),
+                      torch.full((2, D), 1.0 / (256.0 * c), device="cuda"))
+    idx = (torch.arange(T, device="cuda", dtype=torch.int32) % 2)[:, None].contiguous()
+    y = layer.experts(x, idx, torch.ones(T, 1, device="cuda"))
+    h = (128.0 * b).float().cuda()[None].contiguous()
+    q, s = torch.empty(1, F, dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+    moe.moe_quant_i8(h, q, s)
+    want = torch.round(127.0 * b / (254.0 * c))       # ties to even
+    assert torch.equal(q[0].double().cpu(), want) and float(s) == 256.0 * c
+    assert torch.equal(y, q.to(torch.bfloat16).expand(T, F))

@@ -26,12 +26,17 @@
 
 #include "f32x2.cuh"
 #include "host.cuh"
+#include "norm_shape.h"
 
 namespace moe {
 namespace {
 
+using norm_shape::kMaxThreads;
+using norm_shape::kSmallBlock;
+using norm_shape::row_groups;
+using norm_shape::threads_per_row;
+
 constexpr int kMaxD = 8192;          // 1024 threads of 8 columns
-constexpr int kMaxThreads = 1024;
 constexpr int kSms = 148;            // the backward's partial sums are sized for this grid
 constexpr size_t kSmemLimit = 227 * 1024;
 constexpr int kDynSmem = (int)kSmemLimit - 8 * 1024;   // beside the row sums' static 8 KB
@@ -218,8 +223,7 @@ __device__ __forceinline__ float2 centre(F8& v, bool active, const NormArgs& a, 
 // thread of a row holds columns.
 // SMALL: blocks of up to 576 threads in at most 56 registers, so that an SM
 // holds 1168 threads of them (two rows of 4104 columns, not one; three of
-// 2568).
-constexpr int kSmallBlock = 576, kSmallThreads = 1168;
+// 2568); norm_shape.h says which run so.
 template <typename TA, typename TR, bool BIAS, bool FULL, bool SMALL>
 __global__ void __launch_bounds__(SMALL ? kSmallBlock : kMaxThreads, SMALL ? 2 : 1)
 block_norm_kernel(const NormArgs a) {
@@ -703,12 +707,6 @@ int check(const moe_norm_config_t* c) {
 }
 
 bool several_rows(const moe_norm_config_t* c) { return c->gate_len > 0 && c->gate_len < c->T; }
-int threads_per_row(int D) { return (int)(host::ceil_div(D / 8, 32) * 32); }
-// Row groups of a CTA of about `threads` threads (at most 15: a named
-// barrier each; single-warp groups need none, up to 16).
-int row_groups(int tpr, int threads) {
-  return std::max(1, std::min(threads / tpr, tpr == 32 ? 16 : 15));
-}
 // Threads of the backward that share an SM.  LayerNorm's 32 column sums a
 // thread want 80 registers (with 64 they spill: 16384 rows of 4104 bf16 349
 // -> 249 us, of 768 (twice as many) 89 -> 70); fp32 rows, whose rings are
@@ -760,35 +758,19 @@ int with_flags(bool p, bool q, F f) {
 
 template <typename TA, typename TR>
 int forward(NormArgs a, cudaStream_t s) {
-  const int sms = host::sm_count();
-  a.R = row_groups(a.tpr, 256);
-  a.R = (int)std::max<int64_t>(1, std::min<int64_t>(a.R, host::ceil_div(a.T, sms)));
-  const int threads = a.R * a.tpr;
   const bool bias = a.b_post != nullptr || a.b_pre != nullptr;
-  const size_t stage = (size_t)(kPiece<TA> + kPiece<TR>) * threads;
-  size_t fixed = (size_t)threads * 32 * (bias ? 4 : 2);
-  // with biases only where that makes room for another block (the registers
-  // are short there: 16384 x 4104 bf16 228 -> 175 us, but 16384 x 4096 with
-  // an fp32 stream 231 -> 281)
-  const bool small = threads <= kSmallBlock && (!bias || kSmallThreads / threads > 1024 / threads);
-  // 64 registers a thread: 1024 threads of an SM
-  const int per_sm = std::max(1, (small ? kSmallThreads : 1024) / threads);
-  const size_t room = (kSmemLimit + 1024) / per_sm - 9 * 1024;
-  // biases in shared memory only where they leave two rows' room (16384 rows
-  // of 4096 bf16: 142 us with two rows and the biases, 172 with four rows and
-  // the biases read from L2)
-  a.bias_smem = bias && fixed + 2 * stage <= room;
-  if (!a.bias_smem) fixed = (size_t)threads * 64;
-  a.stages = (int)std::max<size_t>(1, std::min<size_t>(4, (room - std::min(room, fixed)) / stage));
-  const size_t smem = a.stages * stage + fixed;
-  const int grid = (int)std::min<int64_t>(host::ceil_div(a.T, a.R), (int64_t)sms * per_sm);
+  const norm_shape::Forward f =
+      norm_shape::forward(a.T, a.D, host::sm_count(), kPiece<TA> + kPiece<TR>, bias);
+  a.R = f.R;
+  a.stages = f.stages;
+  a.bias_smem = f.bias_smem;
   auto go = [&](auto k) {
     MOE_HTRY(host::allow_smem(k, kDynSmem));
-    return host::launch("block_norm", k, grid, threads, smem, s, 1, a);
+    return host::launch("block_norm", k, f.grid, f.threads, (size_t)f.smem, s, 1, a);
   };
-  return with_flags(bias, a.D % 256 == 0, [&](auto b, auto f) {
-    constexpr bool B = decltype(b)::value, F = decltype(f)::value;
-    if (small) return go(block_norm_kernel<TA, TR, B, F, true>);
+  return with_flags(bias, a.D % 256 == 0, [&](auto b, auto full) {
+    constexpr bool B = decltype(b)::value, F = decltype(full)::value;
+    if (f.small) return go(block_norm_kernel<TA, TR, B, F, true>);
     return go(block_norm_kernel<TA, TR, B, F, false>);
   });
 }

@@ -17,7 +17,7 @@ class MoEAdamW:
 
     state    "fp32", or "fp8": e4m3 with a scale for every 256 elements
     masters  keep an fp32 copy of every bf16 parameter and update that
-    no_decay indices of the parameters that weight decay leaves out
+    no_decay indices into params of those that weight decay leaves out
     """
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
@@ -27,10 +27,14 @@ class MoEAdamW:
             raise MoEError("MoEAdamW: %d parameters, %d gradients" % (len(params), len(grads)))
         if state not in ("fp32", "fp8"):
             raise MoEError("MoEAdamW: state is 'fp32' or 'fp8', not %r" % (state,))
+        no_decay = set(no_decay)
+        if not no_decay <= set(range(len(params))):
+            raise MoEError("MoEAdamW: no_decay names parameters that are not there: %r"
+                           % (sorted(no_decay - set(range(len(params))), key=repr),))
         self.cfg = api.make_adamw_config(lr, betas[0], betas[1], eps, weight_decay)
         self.entries = []
         for i, (p, g) in enumerate(zip(params, grads)):
-            e = {"param": p, "grad": g, "decay": i not in set(no_decay)}
+            e = {"param": p, "grad": g, "decay": i not in no_decay}
             if masters and p.dtype == torch.bfloat16:
                 e["master"] = p.float()
             if state == "fp32":

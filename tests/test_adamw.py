@@ -80,3 +80,27 @@ def test_tables_refuse_what_a_step_cannot_take():
     with pytest.raises(C.MoEError):
         MoEAdamW([f], [f], state="int4")
 
+
+
+@pytest.fixture
+def no_gpu_table(monkeypatch):
+    """MoEAdamW on CPU tensors: the table is not described to the library."""
+    monkeypatch.setattr(api, "adamw_table", lambda entries: api.AdamwTable(
+        None, len(entries), torch.device("cpu"), entries))
+
+
+@pytest.mark.parametrize("given", [(1, 3), [3, 1, 1], {1, 3}, "generator"])
+def test_parameters_without_decay(no_gpu_table, given):
+    """no_decay may be any iterable, one that can be read only once too."""
+    from mixture_experts_routing_fp32_b200 import MoEAdamW
+    p = [torch.zeros(4) for _ in range(5)]
+    opt = MoEAdamW(p, p, no_decay=(i for i in (1, 3)) if given == "generator" else given)
+    assert [e["decay"] for e in opt.entries] == [True, False, True, False, True]
+
+
+@pytest.mark.parametrize("bad", [(-1,), (5,), (0, 7), ("w",), (1.5,)])
+def test_no_decay_of_parameters_that_are_not_there_is_refused(no_gpu_table, bad):
+    from mixture_experts_routing_fp32_b200 import MoEAdamW
+    p = [torch.zeros(4) for _ in range(5)]
+    with pytest.raises(C.MoEError, match="no_decay"):
+        MoEAdamW(p, p, no_decay=bad)

@@ -231,7 +231,8 @@ def moe_block_norm(cfg, r, y, w_post, b_post, gate, w_pre, b_pre, r_out, x, stat
         ("stats", stats, f32, 4 * T))), "moe_block_norm")
 
 
-_norm_ws = {}      # workspace bytes by _norm_key
+_norm_ws = {}      # workspace bytes by _norm_key, of up to _NORM_WS_MAX configurations
+_NORM_WS_MAX = 256
 
 
 def _norm_key(cfg):
@@ -243,6 +244,8 @@ def moe_block_norm_ws_bytes(cfg) -> int:
     n = int(lib().moe_block_norm_ws_bytes(ctypes.byref(cfg)))
     if n <= 0:
         check(C.MOE_ERR_ARG, "moe_block_norm_ws_bytes")
+    if len(_norm_ws) >= _NORM_WS_MAX:
+        _norm_ws.clear()
     _norm_ws[_norm_key(cfg)] = n
     return n
 

@@ -129,3 +129,15 @@ def test_reference_gradients_against_differences(norm, post, gate_len, y):
             e.flat[i] = 1e-5
             d = (value({**p, k: p[k] + e}) - value({**p, k: p[k] - e})) / 2e-5
             assert abs(d - grads[name].flat[i]) < 1e-6 * max(1.0, abs(d)), (k, i)
+
+
+def test_workspace_sizes_of_many_configurations_are_not_all_kept(lib):
+    """A batch of another length each step does not make the table grow."""
+    api._norm_ws.clear()
+    sizes = {}
+    for T in range(1, 1500):
+        sizes[T] = api.moe_block_norm_ws_bytes(api.make_norm_config(T, 64, gate_len=7))
+        assert len(api._norm_ws) <= 256
+    for T in (1, 700, 1499):
+        nc = api.make_norm_config(T, 64, gate_len=7)
+        assert api.moe_block_norm_ws_bytes(nc) == sizes[T] == api._norm_ws[api._norm_key(nc)]

@@ -8,7 +8,8 @@
 The block owns the norms' buffers and a MoELayer, all allocated once with
 stable pointers, so a step can be captured in a CUDA graph.  Parameters of a
 forward call that are None are left out (no post norm, gate, biases, next
-norm).  No host synchronisation happens inside forward or backward.
+norm).  A forward keeps references to its inputs: backward needs them as they
+were.  No host synchronisation happens inside forward or backward.
 """
 from __future__ import annotations
 
@@ -17,6 +18,11 @@ import torch
 from . import api
 from ._lib import MoEError
 from .layer import MoELayer
+
+
+def _overlap(a, b):
+    lo, at = a.data_ptr(), b.data_ptr()
+    return lo < at + b.numel() * b.element_size() and at < lo + a.numel() * a.element_size()
 
 
 class MoEBlock:
@@ -55,9 +61,28 @@ class MoEBlock:
                 w_next=None, b_next=None, x=None, **layer_inputs):
         """(r_out, x'), x' None without w_next.  weights: MoELayer.forward's
         (w_r, w13, w_down[, w13_s, w_down_s]); layer_inputs: its other
-        arguments.  Either x (normalised by the block before) or w_pre."""
+        arguments.  Either x (normalised by the block before) or w_pre.
+
+        r may be this block's own r_out, and x its x_next (a block applied
+        again): the outputs are right, but what a backward pass needs is
+        overwritten, so that backward refuses.  The block's other buffers are
+        refused as inputs."""
         if (x is None) == (w_pre is None):
             raise MoEError("MoEBlock.forward: either x or w_pre")
+        # what is written before r, x are read for the last time
+        early = [("layer.y", self.layer.y)] + ([("x", self.x)] if x is None else [])
+        if w_next is not None:
+            early.append(("x_next", self.x_next))
+        for name, t in early:
+            if _overlap(r, t):
+                raise MoEError("MoEBlock.forward: r shares memory with the block's %s" % name)
+        if r.data_ptr() != self.r_out.data_ptr() and _overlap(r, self.r_out):
+            raise MoEError("MoEBlock.forward: r shares memory with a part of the block's r_out")
+        if x is not None and _overlap(x, self.layer.y):
+            raise MoEError("MoEBlock.forward: x shares memory with the block's layer.y")
+        # backward reads x (the layer) or, with w_pre, r (the norm before it)
+        kept = r if x is None else x
+        lost = _overlap(kept, self.r_out) or (w_next is not None and _overlap(kept, self.x_next))
         if x is None:
             api.moe_block_norm(self.pre, r, None, None, None, None, w_pre, b_pre, None, self.x,
                                self.stats_pre)
@@ -68,7 +93,7 @@ class MoEBlock:
         x_next = None if w_next is None else self.x_next
         api.moe_block_norm(self.post, r, y, w_post, b_post, gate, w_next, b_next, self.r_out,
                            x_next, self.stats)
-        self._saved = dict(r=r, y=y, x_given=x is not None, w_pre=w_pre, b_pre=b_pre,
+        self._saved = dict(r=r, y=y, lost=lost, x_given=x is not None, w_pre=w_pre, b_pre=b_pre,
                            w_post=w_post, b_post=b_post, gate=gate, w_next=w_next, b_next=b_next)
         return self.r_out, x_next
 
@@ -96,6 +121,9 @@ class MoEBlock:
         s = self._saved
         if s is None:
             raise MoEError("MoEBlock.backward: no forward before")
+        if s["lost"]:
+            raise MoEError("MoEBlock.backward: the forward overwrote its input (the block's own "
+                           "r_out or x_next); give it a copy")
         if (dx_next is None) != (s["w_next"] is None):
             raise MoEError("MoEBlock.backward: dx_next goes with w_next")
         self._alloc_grads()

@@ -1,0 +1,61 @@
+"""MoEBlock's checks of its inputs (no GPU needed: the block's buffers are CPU
+tensors and the library's calls are left out)."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from mixture_experts_routing_fp32_b200 import MoEBlock, MoEError, api
+
+T, D = 8, 128
+
+
+@pytest.fixture
+def block(monkeypatch):
+    called = []
+    monkeypatch.setattr(api, "moe_block_norm", lambda *a: called.append("norm"))
+    monkeypatch.setattr(api, "moe_block_norm_backward", lambda *a: called.append("back"))
+    b = MoEBlock(api.make_config(T, D, 4, 2, 128), device="cpu")
+    b.layer.forward = lambda *a, **k: b.layer.y
+    b.layer.backward = lambda dy: dy
+    b.called = called
+    return b
+
+
+ONE = torch.ones(D)
+
+
+def rows():
+    return torch.zeros(T, D, dtype=torch.bfloat16)
+
+
+def test_a_block_on_its_own_output_has_no_backward(block):
+    """r = r_out and x = x_next are read before they are written, but not what
+    the backward pass needs of them."""
+    g = rows()
+    for kw, r in ((dict(w_pre=ONE), block.r_out), (dict(x=block.r_out), rows()),
+                  (dict(x=block.x_next, w_next=ONE), rows())):
+        block.forward(r, (), **kw)
+        block.called.clear()
+        with pytest.raises(MoEError, match="overwrote"):
+            block.backward(g, g if "w_next" in kw else None)
+        assert not block.called
+    # neither is written here, or not needed
+    for kw, r in ((dict(x=rows()), block.r_out), (dict(x=block.x_next), rows()),
+                  (dict(x=block.x), rows()), (dict(w_pre=ONE), block.x_next),
+                  (dict(w_pre=ONE, w_next=ONE), rows())):
+        block.forward(r, (), **kw)
+        block.backward(g, g if "w_next" in kw else None)
+
+
+def test_buffers_that_are_written_too_early_are_refused(block):
+    for kw, r in ((dict(w_pre=ONE), block.x), (dict(w_pre=ONE), block.layer.y),
+                  (dict(x=rows()), block.layer.y), (dict(x=block.layer.y), rows()),
+                  (dict(w_pre=ONE, w_next=ONE), block.x_next)):
+        with pytest.raises(MoEError, match="shares memory"):
+            block.forward(r, (), **kw)
+    whole = torch.zeros(T + 1, D, dtype=torch.bfloat16)
+    block.r_out = whole[:T]
+    with pytest.raises(MoEError, match="a part of"):
+        block.forward(whole[1:], (), w_pre=ONE)
+    assert not block.called

@@ -131,3 +131,30 @@ def test_blocks_refuse_what_does_not_fit():
     block.forward(r, w, w_pre=one)
     with pytest.raises(moe.MoEError, match="dx_next"):
         block.backward(r, r)
+
+
+def test_a_block_applied_to_its_own_output():
+    """The outputs of a block that reads its own r_out and x_next are those of
+    copies; its backward, whose inputs are gone, is refused."""
+    import mixture_experts_routing_fp32_b200 as moe
+    cfg = W.REDUCED["mm_b"].replace(T=64)
+    block = moe.MoEBlock(moe.config_from(cfg), alpha=0.5)
+    g = torch.Generator("cuda").manual_seed(1)
+    r = torch.randn(64, cfg.D, generator=g, device="cuda").to(torch.bfloat16)
+    one = torch.ones(cfg.D, device="cuda")
+    w = [W.make_input(cfg, n, "cuda") for n in ("w_r", "w13", "w_down")]
+    first = [t.clone() for t in block.forward(r, w, w_pre=one, w_post=one, w_next=one)]
+    want = [t.clone() for t in block.forward(first[0].clone(), w, x=first[1].clone(), w_post=one,
+                                             w_next=one)]
+    again = [t.clone() for t in block.forward(first[0].clone(), w, w_pre=one, w_post=one)[:1]]
+    block.forward(r, w, w_pre=one, w_post=one, w_next=one)
+    got = block.forward(block.r_out, w, x=block.x_next, w_post=one, w_next=one)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(moe.MoEError, match="overwrote"):
+        block.backward(r, r)
+    block.forward(r, w, w_pre=one, w_post=one)
+    got = block.forward(block.r_out, w, w_pre=one, w_post=one)[0]
+    assert torch.equal(got, again[0])
+    with pytest.raises(moe.MoEError, match="overwrote"):
+        block.backward(r)
+    assert moe.moe_check_status() == 0

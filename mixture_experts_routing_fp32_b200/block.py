@@ -83,6 +83,7 @@ class MoEBlock:
         # backward reads x (the layer) or, with w_pre, r (the norm before it)
         kept = r if x is None else x
         lost = _overlap(kept, self.r_out) or (w_next is not None and _overlap(kept, self.x_next))
+        self._saved = None      # a call that fails from here on leaves no forward
         if x is None:
             api.moe_block_norm(self.pre, r, None, None, None, None, w_pre, b_pre, None, self.x,
                                self.stats_pre)

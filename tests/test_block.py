@@ -59,3 +59,24 @@ def test_buffers_that_are_written_too_early_are_refused(block):
     with pytest.raises(MoEError, match="a part of"):
         block.forward(whole[1:], (), w_pre=ONE)
     assert not block.called
+
+
+def test_a_forward_that_fails_half_way_leaves_no_forward(block, monkeypatch):
+    """Its first launches have rewritten what the forward before it left."""
+    block.forward(rows(), (), w_pre=ONE)
+
+    def refuse(*a, **k):
+        raise MoEError("refused")
+
+    for at in ("layer", "post"):
+        with monkeypatch.context() as m:
+            if at == "layer":
+                m.setattr(block.layer, "forward", refuse)
+            else:
+                m.setattr(api, "moe_block_norm", lambda nc, *a: nc is block.post and refuse())
+            with pytest.raises(MoEError, match="refused"):
+                block.forward(rows(), (), w_pre=ONE)
+        with pytest.raises(MoEError, match="no forward"):
+            block.backward(rows())
+        block.forward(rows(), (), w_pre=ONE)
+        block.backward(rows())

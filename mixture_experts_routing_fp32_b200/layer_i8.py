@@ -93,19 +93,25 @@ class MoEInt8Layer:
             out += [q, s]
         self.set_weights(*out)
 
+    def _inputs(self, x, *specs):
+        """Pointers of x and the other inputs, and the stream; refuses what
+        does not fit the layer."""
+        if self.weights is None:
+            raise MoEError("MoEInt8Layer: no weights (set_weights or quantize first)")
+        c = self.cfg
+        out = api._args("MoEInt8Layer", None, ("x", x, torch.bfloat16, c.T * c.D), *specs)
+        if self.y.get_device() != x.get_device():
+            raise MoEError("MoEInt8Layer: the layer is on %s, x on %s" % (self.device, x.device))
+        return out
+
     def experts(self, x, topk_idx, topk_w, sentinel_mask=None):
         """y [T, D] for given picks (topk_idx [T, K] int32, -1: none; topk_w
         [T, K] fp32): the layer's own buffer, rewritten by the next call."""
-        if self.weights is None:
-            raise MoEError("MoEInt8Layer: no weights (set_weights or quantize first)")
         c, L = self.cfg, lib()
-        xp, idx, w, mask, s = api._args(
-            "MoEInt8Layer", None, ("x", x, torch.bfloat16, c.T * c.D),
-            ("topk_idx", topk_idx, torch.int32, c.T * c.K),
+        xp, idx, w, mask, s = self._inputs(
+            x, ("topk_idx", topk_idx, torch.int32, c.T * c.K),
             ("topk_w", topk_w, torch.float32, c.T * c.K),
             ("sentinel_mask", sentinel_mask, torch.uint8, c.T * c.K))
-        if self.y.get_device() != x.get_device():
-            raise MoEError("MoEInt8Layer: the layer is on %s, x on %s" % (self.device, x.device))
         check(L.moe_dispatch(self._cfg_p, idx, mask, xp, *self._layout, None, self._ws, s),
               "moe_dispatch")
         check(L.moe_expert_ffn_i8(self._cfg_p, xp, *self._map, *self._w, self._o, self._ws_i8, s),
@@ -116,6 +122,12 @@ class MoEInt8Layer:
 
     def forward(self, x, w_r, logit_offset=None, sel_bias=None, sentinel_mask=None):
         """Router (fp32, as MoELayer's) and experts."""
+        c = self.cfg
+        # the router's entry point takes its sizes from cfg alone
+        self._inputs(x, ("w_r", w_r, torch.float32, c.E * c.D),
+                     ("logit_offset", logit_offset, torch.float32, c.E),
+                     ("sel_bias", sel_bias, torch.float32, c.E),
+                     ("sentinel_mask", sentinel_mask, torch.uint8, c.T * c.K))
         api.moe_router(self.cfg, x, w_r, logit_offset, sel_bias, self.logits, self.probs,
                        self.lse, self.topk_idx, self.topk_w, self.near_ties, self.ws)
         return self.experts(x, self.topk_idx, self.topk_w, sentinel_mask)

@@ -97,3 +97,33 @@ def test_blocks_refuse_shards_and_unknown_types():
         MoEBlock(shard, device="cpu")
     with pytest.raises(C.MoEError, match="resid"):
         MoEBlock(api.make_config(64, 128, 8, 2, 128), resid="fp8", device="cpu")
+
+
+@pytest.mark.parametrize("bad", [
+    dict(x=(4, 128)), dict(x=torch.zeros(5, 128)), dict(w_r=(3, 128)),
+    dict(w_r=torch.zeros(4, 128, dtype=torch.bfloat16)), dict(w_r=torch.zeros(128, 4).t()),
+    dict(logit_offset=(3,)), dict(sel_bias=(5, 4)), dict(sel_bias=torch.zeros(4).double()),
+    dict(sentinel_mask=torch.zeros(5, 2)), dict(sentinel_mask=torch.zeros(4, 2, dtype=torch.uint8)),
+])
+def test_a_layer_checks_its_inputs_before_the_router_runs(monkeypatch, bad):
+    """The router takes its sizes from the configuration: a batch of fewer
+    tokens would be read past its end.  (CPU tensors stand for the current
+    device's here, and nothing is launched.)"""
+    from mixture_experts_routing_fp32_b200 import MoEInt8Layer
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    ran = []
+    monkeypatch.setattr(api, "moe_router", lambda *a: ran.append("router"))
+    layer = MoEInt8Layer(api.make_config(**GOOD), device="cpu")
+    monkeypatch.setattr(layer, "experts", lambda *a: ran.append("experts"))
+    good = dict(x=torch.zeros(5, 128, dtype=torch.bfloat16), w_r=torch.zeros(4, 128))
+    with pytest.raises(C.MoEError, match="no weights"):
+        layer.forward(**good)
+    layer.weights = ()
+    with pytest.raises(C.MoEError, match=next(iter(bad)) + " is not"):
+        layer.forward(**{**good, **{k: torch.zeros(v, dtype=good.get(k, good["w_r"]).dtype)
+                                    if isinstance(v, tuple) else v for k, v in bad.items()}})
+    assert not ran
+    layer.forward(**good, sel_bias=torch.zeros(4), logit_offset=torch.zeros(4),
+                  sentinel_mask=torch.zeros(5, 2, dtype=torch.uint8))
+    assert ran == ["router", "experts"]

@@ -69,6 +69,10 @@ class MoEBlock:
         refused as inputs."""
         if (x is None) == (w_pre is None):
             raise MoEError("MoEBlock.forward: either x or w_pre")
+        # the layer's entry points take their sizes from cfg alone
+        n = self.layer.cfg.T * self.layer.cfg.D
+        api._args("MoEBlock.forward", None, ("r", r, self.resid_dtype, n),
+                  ("x", x, self.layer.act_dtype, n))
         # what is written before r, x are read for the last time
         early = [("layer.y", self.layer.y)] + ([("x", self.x)] if x is None else [])
         if w_next is not None:

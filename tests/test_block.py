@@ -12,6 +12,9 @@ T, D = 8, 128
 
 @pytest.fixture
 def block(monkeypatch):
+    # CPU tensors stand for the current device's
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
     called = []
     monkeypatch.setattr(api, "moe_block_norm", lambda *a: called.append("norm"))
     monkeypatch.setattr(api, "moe_block_norm_backward", lambda *a: called.append("back"))
@@ -80,3 +83,17 @@ def test_a_forward_that_fails_half_way_leaves_no_forward(block, monkeypatch):
             block.backward(rows())
         block.forward(rows(), (), w_pre=ONE)
         block.backward(rows())
+
+
+@pytest.mark.parametrize("bad", [
+    torch.zeros(T - 1, D, dtype=torch.bfloat16), torch.zeros(T, D),
+    torch.zeros(D, T, dtype=torch.bfloat16).t(), torch.zeros(T, D, dtype=torch.float16),
+])
+def test_inputs_that_do_not_fit_are_refused_before_the_layer_runs(block, bad):
+    """x goes to the layer, which would read a shorter one past its end."""
+    block.layer.forward = lambda *a, **k: block.called.append("layer")
+    for name, r, kw in (("x", rows(), dict(x=bad)), ("r", bad, dict(x=rows())),
+                        ("r", bad, dict(w_pre=ONE))):
+        with pytest.raises(MoEError, match=name + " is not"):
+            block.forward(r, (), **kw)
+    assert not block.called

@@ -594,9 +594,10 @@ enum { MOE_STATE_FP32 = 0, MOE_STATE_FP8 = 1 };  /* moe_adamw_tensor_t.state */
  *           scaled by blocks of MOE_ADAMW_BLOCK elements: m = m8 * m_scale[b],
  *           sqrt(v) = v8 * v_scale[b] with the largest of the block at 448
  *           (the root halves the range that 8 bits have to span; a positive
- *           v never rounds to zero).  A block whose largest value is below
- *           2^-100 holds zeros.  A NaN or infinity in grad makes its block's
- *           states NaN.
+ *           v never rounds to zero; codes are rounded from v * fl(448 *
+ *           fl(1 / largest)), scales are fl(largest * fl(1 / 448))).  A
+ *           block whose largest value is below 2^-100 holds zeros.  A NaN
+ *           or infinity in grad makes its block's states NaN.
  *   m_scale, v_scale  [ceil(n / MOE_ADAMW_BLOCK)] f32 in/out (NULL for MOE_STATE_FP32)
  *   lr_mult  multiplies lr; decay: 0 or 1, whether weight decay applies
  */

@@ -169,7 +169,10 @@ __device__ __forceinline__ void store_fp8(uint8_t* p, const uint2& u, bool whole
     if (k < n) p[k] = (uint8_t)((k < 4 ? u.x : u.y) >> (8 * (k & 3)));
 }
 // Scale of a block from its largest magnitude, and what its values are
-// multiplied by before rounding.  Not finite: everything becomes NaN.
+// multiplied by before rounding: fl(448 fl(1 / big)) and fl(big fl(1 / 448)),
+// two roundings each, where quotients would take one.  A code is that of the
+// quotient 448 v / big unless that lies within 2^-22 (relative) of a border
+// between two.  Not finite: everything becomes NaN.
 __device__ __forceinline__ float2 block_scale(float big) {
   // (magnitudes order as their bits do, NaN on top)
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
@@ -249,9 +252,10 @@ __device__ __forceinline__ void run_chunk(const Args& a, const Tensor& t, int64_
     v = mul8(v, both(vs));
     v = mul8(v, v);
   }
-  // For 8-bit states products and sums are rounded apart, so that the
-  // roundings to 8 bits below (on which later steps depend) fall as they do
-  // for plain fp32 operations.
+  // For 8-bit states products and sums are rounded apart, as single fp32
+  // operations in the formulas' order round them, so that m' and the root
+  // that are rounded to 8 bits below (on which later steps depend) do not
+  // depend on how they were computed.
   const F8 gm = mul8(g, both(a.omb1)), gv = mul8(mul8(g, both(a.omb2)), g);
   if constexpr (FP8) {
     m = add_apart(mul8(m, both(a.b1)), gm);

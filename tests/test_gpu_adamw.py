@@ -350,3 +350,28 @@ def test_small_eps_and_small_gradients(kind):
         assert (np.abs(update - 1.0) < 1e-3).all()
         tol = want["tol_p"] + HP["lr"] * update * 2.0 ** -149 / want["v"]
         within(e["master"] if "master" in e else e["param"], want["p"], tol, "size %g" % size)
+
+
+def test_8_bit_codes_against_the_quotient():
+    """Codes and scales come from a rounded reciprocal and a product (3 U with
+    the product by the value, 2 U for a scale) where the definition has one
+    quotient: a code is that of 448 v / largest, or of a value 3 U away."""
+    rng = np.random.default_rng(14)
+    n = 256 * 1000
+    e, _ = make(rng, n, dtype="bf16", grad="bf16", state="fp8", fresh=True, master=True)
+    run([e], torch.zeros(2, dtype=torch.int32, device="cuda"))
+    g = e["grad"].float()
+    # fresh states: single fp32 operations in the formulas' order
+    for k, val in (("m", (1 - 0.9) * g), ("v", ((1 - 0.99) * g * g).sqrt())):
+        b = val.double().reshape(-1, BLOCK)
+        top = b.abs().amax(1, keepdim=True)
+        err = (e[k + "_scale"].double() - top[:, 0] / 448).abs()
+        assert bool((err <= 2.01 * U * top[:, 0] / 448).all())
+        at = (448 * b / top).reshape(-1)
+        if k == "v":
+            at = torch.where((at > 0) & (at < 2.0 ** -9), 2.0 ** -9, at)
+        # (the bounds' own rounding to fp32, U more)
+        ends = torch.stack([(at * f).float().to(torch.float8_e4m3fn).float()
+                            for f in (1 - 4.1 * U, 1 + 4.1 * U)])
+        got = e[k].float()
+        assert bool(((ends.amin(0) <= got) & (got <= ends.amax(0))).all())

@@ -323,3 +323,34 @@ def test_h_is_quantised_as_rows_are(T, c):
     want = torch.round(127.0 * b / (254.0 * c))       # ties to even
     assert torch.equal(q[0].double().cpu(), want) and float(s) == 256.0 * c
     assert torch.equal(y, q.to(torch.bfloat16).expand(T, F))
+
+
+@pytest.mark.parametrize("kw", [CASES[4], CASES[7], CASES[11], CASES[15]],
+                         ids=lambda k: "%d-%d" % (k["T"], k["D"]))
+def test_rows_are_rounded_once_and_sums_once(kw):
+    """Of the roundings to bf16 there are two: each row of o, and y, the fp32
+    sum of the rows as they are stored (K + 1 products and sums)."""
+    case = Case(**kw)
+    y = case.run().double()
+    rows = case.layer.slot_row.reshape(case.T, case.K).long()
+    o = case.layer.o.double()
+    x = case.x.double()
+    total, size = torch.zeros_like(x), torch.zeros_like(x)
+    for e in range(case.n):
+        tok, slot = torch.nonzero((case.idx == e + case.base) & (rows >= 0), as_tuple=True)
+        if not tok.numel():
+            continue
+        ref, tol = expert(x[tok], case.w13[0][e], case.w13[1][e], case.wd[0][e], case.wd[1][e])
+        got = o[rows[tok, slot]]
+        assert bool(((got - ref).abs() <= tol * (1 + 2.0 ** -7)).all())
+        part = got * case.w.double()[tok, slot][:, None]
+        total.index_add_(0, tok, part)
+        size.index_add_(0, tok, part.abs())
+    if case.shared:
+        at = int(case.layer.offsets[case.n])
+        got = o[at:at + case.T]
+        ref, tol = expert(x, *case.w13s, *case.wds)
+        assert bool(((got - ref).abs() <= tol * (1 + 2.0 ** -7)).all())
+        total, size = total + got, size + got.abs()
+    tol = 2.0 ** -8 * total.abs() + 2 * (case.K + 1) * U * size
+    assert bool(((y - total).abs() <= tol).all())

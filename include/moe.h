@@ -656,7 +656,7 @@ int64_t moe_expert_ffn_i8_ws_bytes(const moe_config_t* cfg);
  * moe_expert_ffn (no activations are kept for a backward pass).  With
  * q(v), s(v) as moe_quant_i8 gives them for a row v,
  *   [a | b] = s(x) (q(x) w13^T) w13_scale,   h = silu(a) b   (fp32),
- *   o       = s(h) (q(h) w_down^T) w_down_scale
+ *   o       = s(h) (q(h) w_down^T) w_down_scale   (rounded to bf16)
  * the products in integers (exact).  [STA324 §8.1, §8.8]
  *   x          [T,D] act: layer input; each token is quantised once and
  *              its 8-bit row goes to the rows of its slots

@@ -354,3 +354,15 @@ def test_rows_are_rounded_once_and_sums_once(kw):
         total, size = total + got, size + got.abs()
     tol = 2.0 ** -8 * total.abs() + 2 * (case.K + 1) * U * size
     assert bool(((y - total).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("T,E", [(1, 64), (16, 64), (16, 4), (300, 8)])
+def test_an_expert_picked_twice_by_a_token(T, E):
+    """Picks need not differ: the token's rows are computed and added twice
+    (more rows of an expert than tokens, in turns where rows are few)."""
+    case = Case(T, 256, E, 4, 128, seed=T)
+    case.idx[:, 1] = case.idx[:, 0]
+    case.idx[:, 3] = case.idx[:, 0]
+    case.check(case.run())
+    case.idx[:] = 1
+    case.check(case.run())

@@ -19,9 +19,12 @@
 // Each thread copies exactly the 16-byte pieces that it reads back itself,
 // so the ring needs no barrier; the only ones are those of the row sums.
 // Of the copy rate of 6.46 TB/s the bf16 RMSNorm forms reach 91% (forward,
-// 16384 x 4096: 92 us) and 80% (backward, 8192 x 7168: 137 us); LayerNorm
-// with biases, which has twice the row sums, 58% and 55%; RMSNorm of fp32
-// rows (the same shapes) 65% and 70%.
+// 16384 x 4096: 91 us in a replayed graph) and 82% (backward, 8192 x 7168: 134
+// us); LayerNorm with biases, which has twice the row sums, 57% and 55%;
+// RMSNorm of fp32 rows (half as many) 64% and 73%, of bf16 rows beside an fp32
+// stream 73% and 61%.  Gate rows of a few tokens are the slowest form (65536 x
+// 256 backward: 42 us without a gate, 71 with 16 tokens a gate row, 183 with 4,
+// 292 with one): their CTAs run one row group and meet at every gate row's end.
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -791,8 +794,11 @@ int backward(NormArgs a, int P, bool bias, cudaStream_t s) {
   const size_t w_bytes = (general ? 2 : 1) * (size_t)a.D * 4;
   a.w_smem = a.several && fixed + w_bytes + 2 * stage <= room;
   if (a.w_smem) fixed += w_bytes;
-  // a ring of one stage would overlap nothing: rows too long for two (wide
-  // fp32 rows) are read where they are used
+  // a ring of one stage would overlap nothing: where two do not fit, rows are
+  // read where they are used.  That is so for fp32 rows of most widths (at 768
+  // and 2048 columns two CTAs of about 500 threads have 105 KB each and a stage
+  // takes 60 to 64; at 7168 one CTA has 219 KB and a stage takes 112), and for
+  // an fp32 stream beside bf16 rows of 4096
   a.stages = (int)std::min<size_t>(3, (room - fixed) / stage);
   if (a.stages < 2) a.stages = 0;
   a.swap_ring = !a.several && a.stages > 0;      // (a stage is at least the buffer's size)

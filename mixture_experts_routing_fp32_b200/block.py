@@ -69,6 +69,8 @@ class MoEBlock:
         refused as inputs."""
         if (x is None) == (w_pre is None):
             raise MoEError("MoEBlock.forward: either x or w_pre")
+        if r is None:
+            raise MoEError("MoEBlock.forward: no r")
         # the layer's entry points take their sizes from cfg alone
         n = self.layer.cfg.T * self.layer.cfg.D
         api._args("MoEBlock.forward", None, ("r", r, self.resid_dtype, n),

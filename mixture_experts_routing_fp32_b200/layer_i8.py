@@ -98,6 +98,8 @@ class MoEInt8Layer:
         does not fit the layer."""
         if self.weights is None:
             raise MoEError("MoEInt8Layer: no weights (set_weights or quantize first)")
+        if x is None:
+            raise MoEError("MoEInt8Layer: no x")
         c = self.cfg
         out = api._args("MoEInt8Layer", None, ("x", x, torch.bfloat16, c.T * c.D), *specs)
         if self.y.get_device() != x.get_device():

@@ -97,3 +97,16 @@ def test_inputs_that_do_not_fit_are_refused_before_the_layer_runs(block, bad):
         with pytest.raises(MoEError, match=name + " is not"):
             block.forward(r, (), **kw)
     assert not block.called
+
+
+def test_a_missing_input_is_refused_by_name(block):
+    from mixture_experts_routing_fp32_b200 import MoEInt8Layer
+    for kw in (dict(w_pre=ONE), dict(x=rows())):
+        with pytest.raises(MoEError, match="no r"):
+            block.forward(None, (), **kw)
+    layer = MoEInt8Layer(api.make_config(T, D, 4, 2, 128), device="cpu")
+    layer.weights = ()
+    for call in (lambda: layer.forward(None, torch.zeros(4, D)),
+                 lambda: layer.experts(None, None, None)):
+        with pytest.raises(MoEError, match="no x"):
+            call()

@@ -158,3 +158,52 @@ def test_a_block_applied_to_its_own_output():
     with pytest.raises(moe.MoEError, match="overwrote"):
         block.backward(r)
     assert moe.moe_check_status() == 0
+
+
+def test_a_block_and_its_served_form_in_graphs():
+    """Forward and backward of a block, and the 8-bit layer with its router,
+    captured once and replayed on other inputs: the bits of eager calls."""
+    import mixture_experts_routing_fp32_b200 as moe
+    cfg = W.REDUCED["olmoe"].replace(T=300, sentinel_frac=0.0)
+    T, D = cfg.T, cfg.D
+    w = [W.make_input(cfg, n, "cuda") for n in ("w_r", "w13", "w_down")]
+    g = torch.Generator("cuda").manual_seed(3)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
+    vec = {k: 1 + 0.2 * rand(D) for k in ("w_pre", "w_post", "w_next")}
+    vec.update(b_pre=rand(D), b_post=rand(D), b_next=rand(D), gate=rand(-(-T // 70), D))
+    rows = lambda: rand(T, D).to(torch.bfloat16)  # noqa: E731
+    r, dr, dx = rows(), rows(), rows()
+    block = moe.MoEBlock(moe.config_from(cfg), norm="layer", alpha=0.5, gate_len=70)
+    served = moe.MoEInt8Layer(moe.config_from(cfg))
+    served.quantize(w[1], w[2])
+
+    def step():
+        block.forward(r, w, **vec)
+        block.backward(dr, dx)
+        served.forward(block.x, w[0])
+
+    def results():
+        b = block
+        return [t.clone() for t in (
+            b.r_out, b.x_next, b.dr, b.dy, b.dw_pre, b.db_pre, b.dw_post, b.db_post, b.dw_next,
+            b.db_next, b.dgate, b.layer.dw_r, b.layer.dw13, b.layer.dw_down, served.y)]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    for t in (r, dr, dx):
+        t.copy_(rows())
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = results()
+    step()
+    torch.cuda.synchronize()
+    for a, b in zip(got, results()):
+        assert bool(torch.isfinite(a.float()).all()) and torch.equal(a, b)
+    assert moe.moe_check_status() == 0
